@@ -233,9 +233,147 @@ muon_status muon_ns_phase_run(muon_handle* h, const muon_ns_phase_args* args, vo
 muon_status muon_qk_clip(muon_handle* h, float* Wq, float* Wk, const float* max_logits, int n_heads, int head_dim,
                          int cols, float tau, void* stream);
 
+/* QK-Clip of a layer whose query heads share key heads (grouped heads: query head h
+ * reads key head h / (n_heads / n_kv_heads)).  With gamma_h = min(1, tau / max_logits[h]),
+ * the rows of key head g are multiplied by kappa_g = sqrt(smallest gamma_h of its
+ * group) and the rows of query head h by gamma_h / kappa_g, so that every logit of
+ * head h scales by exactly gamma_h and the shared key rows by one factor.  With
+ * n_kv_heads == n_heads it is muon_qk_clip.  Wq: fp32 (n_heads*head_dim) x cols, Wk:
+ * fp32 (n_kv_heads*head_dim) x cols, both required, row-major, device, updated in
+ * place; max_logits: n_heads floats, device (muon_attention writes them); a NaN
+ * entry clips nothing; tau > 0. */
+muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const float* max_logits, int n_heads,
+                                 int n_kv_heads, int head_dim, int cols, float tau, void* stream);
+
+/* ---- operators between a layer's forward pass and its Muon step ---------------
+ * They keep no state on the handle: every buffer is the caller's, so calls on
+ * several streams, and captured graphs replayed side by side, do not meet.  They
+ * can be captured in a caller's CUDA graph at the first call. */
+
+/* A bf16 device array of `heads` vectors of head_dim elements for each row (token):
+ * element d of head h of row r is at ptr[r*row_stride + h*head_stride + d] (strides in
+ * elements).  Rows x heads or heads x rows, dense or a view of a larger array (the
+ * q, k and v parts of one fused projection): ptr 16-byte aligned, strides multiples
+ * of 8 elements (a stride over a single row or head is not looked at), and no two
+ * vectors may overlap. */
+typedef struct {
+    void* ptr;
+    long long row_stride, head_stride;
+} muon_heads;
+
+/* Causal attention over packed sequences with grouped heads, as the model's forward
+ * pass computes it, and the largest logit of every head, which muon_qk_clip needs.
+ * Sequence s has the query rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1 of q and out
+ * and the key rows cu_seqlens_k[s] .. cu_seqlens_k[s+1]-1 of k and v (both int32,
+ * device, n_seqs + 1 entries, non-decreasing, between 0 and total_q / total_k;
+ * usually the same array).  Query i of a sequence with Lq queries and Lk keys sees
+ * its keys j <= i + Lk - Lq: the last query sees every key.  Query head h reads key
+ * head h / (n_heads / n_kv_heads).
+ *
+ *   S_ij = scale * q_i . k_j      O_i = sum_j exp(S_ij - lse_i) v_j
+ *   lse_i = log sum_j exp(S_ij)   max_logits[h] = max(max_logits[h], max_ij S_ij)
+ *
+ * A query that sees no key gets O = 0 and lse = -inf.  Rows that belong to no
+ * sequence (between sequences, behind the last) are not written.  Sums, softmax
+ * statistics and products are accumulated in fp32; the exponentials enter the second
+ * product rounded to bf16.
+ *
+ * head_dim: a multiple of 8, at most 128.  scale: finite and > 0.  q, k, v: read; out:
+ * written; lse: fp32 [n_heads][total_q], written; max_logits: n_heads floats or NULL,
+ * updated in place (start an optimizer step's micro-batches from -inf; a NaN logit is
+ * passed over).  out, lse and max_logits may not overlap any buffer of the call
+ * (strided views that interleave without sharing an element do not overlap).
+ * Non-finite values in a sequence's own rows reach its outputs; the values of one
+ * sequence, and of rows in none, never reach another's.
+ * cu_seqlens values outside the rule above are seen by the kernels only: such a
+ * sequence is passed over, and muon_sync reports MUON_ERR_INVALID. */
+typedef struct {
+    int n_seqs, n_heads, n_kv_heads, head_dim;
+    int total_q, total_k;            /* rows of q / out / lse and of k / v */
+    const int32_t* cu_seqlens_q;
+    const int32_t* cu_seqlens_k;
+    float scale;
+    muon_heads q, k, v;
+    muon_heads out;
+    float* lse;
+    float* max_logits;
+} muon_attention_args;
+
+/* Host-only check, usable without a GPU.  MUON_OK, MUON_ERR_INVALID or
+ * MUON_ERR_UNSUPPORTED (a head_dim or alignment that the kernels do not take). */
+muon_status muon_validate_attention(const muon_attention_args* args);
+muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void* stream);
+
+/* Gradients of muon_attention: with out and lse as the forward call left them (read
+ * here) and grad_out = dL/dO, with D_i = grad_out_i . O_i and P_ij = exp(S_ij - lse_i),
+ *
+ *   dS_ij = P_ij (grad_out_i . v_j - D_i)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij grad_out_i
+ *
+ * dk and dv are summed in fp32 over the query heads that share a key head.  No
+ * atomics: the same inputs give the same bits.  forward.max_logits is not looked at.
+ * grad_out: layout of out; dq, dk, dv: layouts of q, k, v, written (rows of no
+ * sequence are not; keys that no query sees get zero).  delta: scratch for
+ * n_heads * total_q floats, written.  P and dS enter their products rounded to bf16.
+ * dq, dk, dv and delta may not overlap any buffer of the call. */
+typedef struct {
+    muon_attention_args forward;
+    muon_heads grad_out;
+    muon_heads dq, dk, dv;
+    float* delta;
+} muon_attention_grad_args;
+
+muon_status muon_validate_attention_grad(const muon_attention_grad_args* args);
+muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_args* args, void* stream);
+
+/* An activation x (rows x cols) kept in 8 bits until the backward pass: blocks of
+ * MUON_CKPT_BLOCK values along a row share a scale byte E, and a value is
+ * code * 2^(E - 133) with an int8 code.  E is the smallest E >= 0 for which every
+ * code of the block, rounded to nearest even, stays within +-127 (so a value is off
+ * by at most half a unit, 1/127 of the block's largest magnitude); it is at most 254,
+ * where codes saturate.  A block that holds an infinity or NaN gets E = 255 and reads
+ * back as NaN throughout.  Every stored value is exact in bf16 and in fp32.
+ * codes: int8 [rows][ld], scales: uint8 [rows][ld / MUON_CKPT_BLOCK], both dense, with
+ * ld = cols rounded up to a multiple of MUON_CKPT_BLOCK (the padding codes are
+ * written as 0); codes 16-byte aligned.  x: bf16 or fp32, device, row r at
+ * x + r * x_stride elements, x_stride >= cols. */
+#define MUON_CKPT_BLOCK 32
+muon_status muon_checkpoint_store(muon_handle* h, const void* x, int x_dtype, int rows, int cols, long long x_stride,
+                                  int8_t* codes, uint8_t* scales, void* stream);
+/* Reads it back: x (rows x cols, bf16 or fp32) = code * 2^(E - 133). */
+muon_status muon_checkpoint_load(muon_handle* h, const int8_t* codes, const uint8_t* scales, int rows, int cols,
+                                 void* x, int x_dtype, long long x_stride, void* stream);
+
+/* The gradient of a linear layer's weight, taken from its input's 8-bit checkpoint:
+ * for y = x W^T with W rows x cols,  G = dy^T x^  (accumulate = 0)  or  G += dy^T x^
+ * (accumulate = 1), x^ the value of the checkpoint (tokens x cols) and dy the bf16
+ * gradient of y (tokens x rows; row t at dy + t * dy_stride elements, dy_stride >= rows).
+ * G is the rows x cols gradient that muon_step reads, fp32 or bf16, dense; sums are
+ * fp32 and G is rounded once.  tokens may be 0.  workspace: device scratch of at least
+ * muon_weight_grad_workspace() bytes, 16-byte aligned (NULL when that is 0).  The same
+ * inputs give the same bits. */
+typedef struct {
+    int tokens, rows, cols;
+    const void* dy;
+    long long dy_stride;
+    const int8_t* codes;
+    const uint8_t* scales;
+    void* G;
+    int grad_dtype;          /* muon_dtype of G */
+    int accumulate;          /* 0 or 1 */
+    void* workspace;
+    size_t workspace_bytes;
+} muon_weight_grad_args;
+
+/* Host-only; the first also works with the pointers unset (workspace size of the shape). */
+muon_status muon_weight_grad_workspace(const muon_weight_grad_args* args, size_t* bytes);
+muon_status muon_validate_weight_grad(const muon_weight_grad_args* args);
+muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* args, void* stream);
+
 /* Waits for the handle's work on `stream`, then reports a kernel that gave up a
- * bounded wait (MUON_ERR_DEVICE_TIMEOUT, flag cleared) or an asynchronous CUDA
- * error (MUON_ERR_CUDA). */
+ * bounded wait (MUON_ERR_DEVICE_TIMEOUT, flag cleared), one that met cu_seqlens out of
+ * range (MUON_ERR_INVALID, flag cleared) or an asynchronous CUDA error
+ * (MUON_ERR_CUDA). */
 muon_status muon_sync(muon_handle* h, void* stream);
 
 /* Copies the Frobenius norms ||U||_F of the last step's matrices (groups in

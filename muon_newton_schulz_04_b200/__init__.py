@@ -66,6 +66,30 @@ class _PhaseArgs(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("out_op", ctypes.c_void_p)]
 
 
+class _Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("total_q", ctypes.c_int), ("total_k", ctypes.c_int),
+                ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("q", _Heads), ("k", _Heads), ("v", _Heads), ("out", _Heads),
+                ("lse", ctypes.c_void_p), ("max_logits", ctypes.c_void_p)]
+
+
+class _AttentionGradArgs(ctypes.Structure):
+    _fields_ = [("forward", _AttentionArgs), ("grad_out", _Heads), ("dq", _Heads), ("dk", _Heads), ("dv", _Heads),
+                ("delta", ctypes.c_void_p)]
+
+
+class _WeightGradArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("dy", ctypes.c_void_p),
+                ("dy_stride", ctypes.c_longlong), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("G", ctypes.c_void_p), ("grad_dtype", ctypes.c_int), ("accumulate", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _LIB: Optional[ctypes.CDLL] = None
 
 # name -> (restype, argtypes)
@@ -85,6 +109,21 @@ _SIGNATURES = {
     "muon_ns_phase_run": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_PhaseArgs), ctypes.c_void_p]),
     "muon_qk_clip": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                     ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p]),
+    "muon_qk_clip_grouped": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                                            ctypes.c_void_p]),
+    "muon_validate_attention": (ctypes.c_int, [ctypes.POINTER(_AttentionArgs)]),
+    "muon_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionArgs), ctypes.c_void_p]),
+    "muon_validate_attention_grad": (ctypes.c_int, [ctypes.POINTER(_AttentionGradArgs)]),
+    "muon_attention_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionGradArgs), ctypes.c_void_p]),
+    "muon_checkpoint_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                             ctypes.c_longlong, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "muon_checkpoint_load": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                            ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong,
+                                            ctypes.c_void_p]),
+    "muon_weight_grad_workspace": (ctypes.c_int, [ctypes.POINTER(_WeightGradArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    "muon_validate_weight_grad": (ctypes.c_int, [ctypes.POINTER(_WeightGradArgs)]),
+    "muon_weight_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_WeightGradArgs), ctypes.c_void_p]),
     "muon_sync": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "muon_last_norms": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_float), ctypes.c_int,
                                        ctypes.POINTER(ctypes.c_int), ctypes.c_void_p]),
@@ -153,6 +192,59 @@ class Group:
     scale: float = 1.0
 
 
+CKPT_BLOCK = 32     # values of an 8-bit checkpoint that share a scale
+
+
+@dataclasses.dataclass
+class Checkpoint:
+    """An activation in 8 bits (see muon_checkpoint_store): codes int8 [rows, cols rounded up to CKPT_BLOCK],
+    scales uint8 [rows, that / CKPT_BLOCK]; value = code * 2**(scale - 133), NaN where the scale is 255."""
+    codes: object
+    scales: object
+    cols: int
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "Checkpoint":
+        import torch
+        blocks = -(-cols // CKPT_BLOCK)
+        return Checkpoint(torch.empty(rows, blocks * CKPT_BLOCK, dtype=torch.int8, device=device),
+                          torch.empty(rows, blocks, dtype=torch.uint8, device=device), cols)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def _check_checkpoint(ckpt: Checkpoint, device: int):
+    import torch
+    blocks = -(-ckpt.cols // CKPT_BLOCK)
+    _check_tensors([ckpt.codes], (ckpt.rows, blocks * CKPT_BLOCK), True, torch.int8, device)
+    _check_tensors([ckpt.scales], (ckpt.rows, blocks), True, torch.uint8, device)
+
+
+def _check_heads(name: str, t, shape, device: int):
+    """A bf16 CUDA tensor [rows, heads, head_dim] of the given shape with a dense last dimension."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected torch.bfloat16")
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _check_rows(name: str, t, device: int):
+    """A 2-D CUDA tensor with dense rows; returns its row stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with dense rows")
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    return t.stride(0)
+
+
 def _ptrs(ts) -> "ctypes.Array":
     arr = (ctypes.c_void_p * len(ts))()
     for i, t in enumerate(ts):
@@ -191,6 +283,17 @@ def _stream(stream, device: Optional[int] = None) -> int:
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on_stream(stream, device: int):
+    """Context in which torch allocates for work on `stream` (a torch stream, a raw cudaStream_t or None)."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Muon:
@@ -346,6 +449,141 @@ class Muon:
                                        None if Wk is None else ctypes.c_void_p(Wk.data_ptr()),
                                        ctypes.c_void_p(max_logits.data_ptr()), n_heads, head_dim, cols, float(tau),
                                        ctypes.c_void_p(_stream(stream, self.device))), "muon_qk_clip")
+
+    def qk_clip_grouped(self, Wq, Wk, max_logits, head_dim: int, tau: float, stream=None):
+        """QK-Clip of a layer whose query heads share key heads (see muon_qk_clip_grouped): Wq fp32
+        (n_heads * head_dim) x cols, Wk fp32 (n_kv_heads * head_dim) x cols, max_logits as `attention` leaves it."""
+        import torch
+        for name, t in (("Wq", Wq), ("Wk", Wk), ("max_logits", max_logits)):
+            if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
+            if t.device.index != self.device:
+                raise ValueError(f"{name} is on cuda:{t.device.index}, the handle on cuda:{self.device}")
+        n_heads = max_logits.numel()
+        if Wq.dim() != 2 or Wk.dim() != 2 or Wq.shape[1] != Wk.shape[1]:
+            raise ValueError("Wq and Wk must be 2-D with the same number of columns")
+        if head_dim <= 0 or Wq.shape[0] != n_heads * head_dim or Wk.shape[0] % head_dim != 0 or Wk.shape[0] == 0:
+            raise ValueError("Wq must have n_heads * head_dim rows, Wk a multiple of head_dim")
+        self._check(lib().muon_qk_clip_grouped(self._h, Wq.data_ptr(), Wk.data_ptr(), max_logits.data_ptr(), n_heads,
+                                               Wk.shape[0] // head_dim, head_dim, Wq.shape[1], float(tau),
+                                               ctypes.c_void_p(_stream(stream, self.device))), "muon_qk_clip_grouped")
+
+    def _attention_args(self, q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits):
+        import torch
+        if q.dim() != 3 or k.dim() != 3:
+            raise ValueError("q and k must be [rows, heads, head_dim]")
+        (tq, hq, d), (tk, hk, _) = q.shape, k.shape
+        cu_k = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
+        for name, t in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_k)):
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+            if t.device.index != self.device:
+                raise ValueError(f"{name} is on {t.device}, the handle on cuda:{self.device}")
+            if t.numel() != cu_seqlens.numel() or t.numel() < 1:
+                raise ValueError("cu_seqlens and cu_seqlens_k must hold one entry more than there are sequences")
+        _check_tensors([lse], (hq, tq), True, torch.float32, self.device)
+        if max_logits is not None:
+            _check_tensors([max_logits], (hq,), True, torch.float32, self.device)
+        return _AttentionArgs(cu_seqlens.numel() - 1, hq, hk, d, tq, tk, cu_seqlens.data_ptr(), cu_k.data_ptr(),
+                              d ** -0.5 if scale is None else float(scale),
+                              _check_heads("q", q, (tq, hq, d), self.device),
+                              _check_heads("k", k, (tk, hk, d), self.device),
+                              _check_heads("v", v, (tk, hk, d), self.device),
+                              _check_heads("out", out, (tq, hq, d), self.device), lse.data_ptr(),
+                              None if max_logits is None else max_logits.data_ptr())
+
+    def attention(self, q, k, v, cu_seqlens, out=None, lse=None, max_logits=None, scale: Optional[float] = None,
+                  cu_seqlens_k=None, stream=None):
+        """Causal attention over packed sequences (see muon_attention): q [rows, heads, head_dim] and k, v
+        [rows, kv heads, head_dim] in bf16, cu_seqlens int32 [sequences + 1] on the device (cu_seqlens_k where the
+        keys are packed otherwise), scale 1 / sqrt(head_dim) by default.  Writes out (layout of q), lse
+        [heads, rows] fp32 and raises max_logits [heads] fp32 to the largest logit of each head, for qk_clip.
+        Returns (out, lse); buffers that are not given are allocated, rows of no sequence left as they are."""
+        import torch
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if lse is None:
+                lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+        args = self._attention_args(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits)
+        self._check(lib().muon_attention(self._h, ctypes.byref(args), ctypes.c_void_p(_stream(stream, self.device))),
+                    "muon_attention")
+        return out, lse
+
+    def attention_backward(self, grad_out, q, k, v, out, lse, cu_seqlens, dq=None, dk=None, dv=None,
+                           scale: Optional[float] = None, cu_seqlens_k=None, stream=None):
+        """Gradients of `attention` (see muon_attention_backward) from its inputs, out and lse.  Returns
+        (dq, dk, dv); buffers that are not given are allocated, rows of no sequence left as they are."""
+        import torch
+        with torch.cuda.device(self.device), _on_stream(stream, self.device):
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+            delta = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+        fwd = self._attention_args(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, None)
+        args = _AttentionGradArgs(fwd, _check_heads("grad_out", grad_out, q.shape, self.device),
+                                  _check_heads("dq", dq, q.shape, self.device),
+                                  _check_heads("dk", dk, k.shape, self.device),
+                                  _check_heads("dv", dv, k.shape, self.device), delta.data_ptr())
+        self._check(lib().muon_attention_backward(self._h, ctypes.byref(args),
+                                                  ctypes.c_void_p(_stream(stream, self.device))),
+                    "muon_attention_backward")
+        return dq, dk, dv
+
+    def checkpoint(self, x, ckpt: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
+        """x (2-D, bf16 or fp32, dense rows) in 8 bits, for the backward pass (see muon_checkpoint_store)."""
+        import torch
+        stride = _check_rows("x", x, self.device)
+        if ckpt is None:
+            with torch.cuda.device(self.device), _on_stream(stream, self.device):
+                ckpt = Checkpoint.empty(x.shape[0], x.shape[1], x.device)
+        _check_checkpoint(ckpt, self.device)
+        if (ckpt.rows, ckpt.cols) != tuple(x.shape):
+            raise ValueError(f"the checkpoint holds {ckpt.rows} x {ckpt.cols} values, x is {tuple(x.shape)}")
+        self._check(lib().muon_checkpoint_store(self._h, x.data_ptr(), _dtype_code(x), x.shape[0], x.shape[1], stride,
+                                                ckpt.codes.data_ptr(), ckpt.scales.data_ptr(),
+                                                ctypes.c_void_p(_stream(stream, self.device))),
+                    "muon_checkpoint_store")
+        return ckpt
+
+    def checkpoint_load(self, ckpt: Checkpoint, out=None, stream=None):
+        """The values of a checkpoint, written to `out` (bf16 or fp32, dense rows; bf16 when not given)."""
+        import torch
+        _check_checkpoint(ckpt, self.device)
+        if out is None:
+            with torch.cuda.device(self.device), _on_stream(stream, self.device):
+                out = torch.empty(ckpt.rows, ckpt.cols, dtype=torch.bfloat16, device=ckpt.codes.device)
+        stride = _check_rows("out", out, self.device)
+        if tuple(out.shape) != (ckpt.rows, ckpt.cols):
+            raise ValueError(f"the checkpoint holds {ckpt.rows} x {ckpt.cols} values, out is {tuple(out.shape)}")
+        self._check(lib().muon_checkpoint_load(self._h, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ckpt.rows,
+                                               ckpt.cols, out.data_ptr(), _dtype_code(out), stride,
+                                               ctypes.c_void_p(_stream(stream, self.device))), "muon_checkpoint_load")
+        return out
+
+    def weight_grad(self, dy, ckpt: Checkpoint, G, accumulate: bool = False, stream=None):
+        """G = dy^T x^ (or G += with `accumulate`): the gradient of the weight of y = x W^T from the checkpoint of x
+        (see muon_weight_grad).  dy bf16 [tokens, rows] with dense rows; G fp32 or bf16 [rows, cols], the gradient
+        that `step` takes.  Returns G."""
+        import torch
+        _check_checkpoint(ckpt, self.device)
+        stride = _check_rows("dy", dy, self.device)
+        if dy.dtype != torch.bfloat16:
+            raise TypeError(f"dy: unsupported dtype {dy.dtype}, expected torch.bfloat16")
+        if dy.shape[0] != ckpt.rows:
+            raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {ckpt.rows}")
+        _check_tensors([G], (dy.shape[1], ckpt.cols), True, None, self.device)
+        args = _WeightGradArgs(dy.shape[0], dy.shape[1], ckpt.cols, dy.data_ptr(), stride, ckpt.codes.data_ptr(),
+                               ckpt.scales.data_ptr(), G.data_ptr(), _dtype_code(G), int(accumulate), None, 0)
+        need = ctypes.c_size_t(0)
+        st = lib().muon_weight_grad_workspace(ctypes.byref(args), ctypes.byref(need))
+        if st == MUON_OK and need.value:
+            with torch.cuda.device(self.device), _on_stream(stream, self.device):
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=G.device)
+            args.workspace, args.workspace_bytes = workspace.data_ptr(), need.value
+        self._check(lib().muon_weight_grad(self._h, ctypes.byref(args), ctypes.c_void_p(_stream(stream, self.device))),
+                    "muon_weight_grad")
+        return G
 
     def sync(self, stream=None):
         self._check(lib().muon_sync(self._h, ctypes.c_void_p(_stream(stream, self.device))), "muon_sync")

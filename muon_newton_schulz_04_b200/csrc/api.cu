@@ -23,6 +23,7 @@
 
 #include "../../include/muon.h"
 #include "kernels.cuh"
+#include "model_ops.cuh"
 #include "plan.h"
 
 using namespace muon;
@@ -287,6 +288,193 @@ muon_status check_groups(const muon_group* g, int n, std::string* why) {
         }
     }
     return check_spans(sp, why);
+}
+
+// ---- operators between a layer's forward pass and its step: host checks ----
+
+// Bytes [base, base + extent) that a strided array of a call touches; when row > 0 it
+// touches only [base + i * row, + width) for i < rows, width <= row.
+struct Extent {
+    uintptr_t base = 0;
+    size_t extent = 0, row = 0, width = 0;
+    bool written = false;
+    const char* name = "";
+};
+
+Extent flat(const void* p, size_t bytes, bool written, const char* name) {
+    return Extent{reinterpret_cast<uintptr_t>(p), bytes, 0, 0, written, name};
+}
+
+bool share_memory(const Extent& x, const Extent& y) {
+    const Extent &a = x.base <= y.base ? x : y, &b = x.base <= y.base ? y : x;
+    if (a.extent == 0 || b.extent == 0 || a.base + a.extent <= b.base) return false;
+    // views of one row-major array: disjoint column ranges do not meet
+    if (a.row > 0 && a.row == b.row) {
+        const size_t off = (b.base - a.base) % a.row;
+        if (off >= a.width && off + b.width <= a.row) return false;
+    }
+    return true;
+}
+
+muon_status check_extents(const Extent* e, int n, std::string* why) {
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if ((e[i].written || e[j].written) && share_memory(e[i], e[j])) {
+                *why = std::string(e[i].name) + " and " + e[j].name + " share memory, and the call writes one of them";
+                return MUON_ERR_INVALID;
+            }
+    return MUON_OK;
+}
+
+// A rows x heads array of head_dim bf16 vectors: 16-byte addresses throughout (TMA), no
+// two vectors overlapping.  Strides over one row or head are not looked at.
+muon_status check_heads(const muon_heads& v, int rows, int heads, int d, bool written, const char* name, Extent* e,
+                        std::string* why) {
+    *e = Extent{};
+    e->name = name;
+    if (rows == 0) return MUON_OK;
+    if (!v.ptr) { *why = std::string(name) + " is NULL"; return MUON_ERR_INVALID; }
+    const long long rs = rows > 1 ? v.row_stride : 0, hs = heads > 1 ? v.head_stride : 0;
+    if (rs < 0 || hs < 0 || rs >= (1ll << 38) || hs >= (1ll << 38)) {
+        *why = std::string(name) + ": strides must be positive and below 2^38";
+        return MUON_ERR_INVALID;
+    }
+    const bool by_row = (heads == 1 || hs >= d) && (rows == 1 || rs >= (heads - 1) * hs + d);
+    const bool by_head = (rows == 1 || rs >= d) && (heads == 1 || hs >= (rows - 1) * rs + d);
+    if (!by_row && !by_head) { *why = std::string(name) + ": vectors overlap"; return MUON_ERR_INVALID; }
+    if (!aligned(v.ptr, 16) || rs % 8 != 0 || hs % 8 != 0) {
+        *why = std::string(name) + ": needs a 16-byte aligned pointer and strides that are multiples of 8 elements";
+        return MUON_ERR_UNSUPPORTED;
+    }
+    *e = flat(v.ptr, 2 * (size_t)((rows - 1) * rs + (heads - 1) * hs + d), written, name);
+    if (by_row && rows > 1) { e->row = 2 * (size_t)rs; e->width = 2 * (size_t)((heads - 1) * hs + d); }
+    return MUON_OK;
+}
+
+// Fills e[0..8) with the buffers of the call; out_written: the forward call's outputs.
+muon_status check_attention(const muon_attention_args* a, bool forward, Extent* e, std::string* why) {
+    if (!a) { *why = "args is NULL"; return MUON_ERR_INVALID; }
+    if (a->n_seqs < 0 || a->total_q < 0 || a->total_k < 0 || a->n_heads <= 0 || a->n_kv_heads <= 0 || a->head_dim <= 0) {
+        *why = "n_heads, n_kv_heads and head_dim must be > 0, n_seqs, total_q and total_k >= 0";
+        return MUON_ERR_INVALID;
+    }
+    if (a->n_heads % a->n_kv_heads != 0) { *why = "n_heads must be a multiple of n_kv_heads"; return MUON_ERR_INVALID; }
+    if (!(finite(a->scale) && a->scale > 0.f)) { *why = "scale must be finite and > 0"; return MUON_ERR_INVALID; }
+    if (a->head_dim % 8 != 0 || a->head_dim > 128) { *why = "head_dim must be a multiple of 8, at most 128"; return MUON_ERR_UNSUPPORTED; }
+    if (a->n_heads > 32768 || a->n_seqs > (1 << 24) || a->total_q > (1 << 30) || a->total_k > (1 << 30) ||
+        ((long long)a->total_q / 128 + a->n_seqs + 1) * a->n_heads > (1ll << 31) - 1 ||
+        ((long long)a->total_k / 128 + a->n_seqs + 1) * a->n_heads > (1ll << 31) - 1) {
+        *why = "too many heads, sequences or rows";
+        return MUON_ERR_UNSUPPORTED;
+    }
+    if (a->n_seqs > 0 && (!a->cu_seqlens_q || !a->cu_seqlens_k)) { *why = "cu_seqlens is NULL"; return MUON_ERR_INVALID; }
+    if (!aligned(a->cu_seqlens_q, 4) || !aligned(a->cu_seqlens_k, 4) || !aligned(a->lse, 4) || !aligned(a->max_logits, 4)) {
+        *why = "misaligned pointer";
+        return MUON_ERR_INVALID;
+    }
+    if (a->total_q > 0 && !a->lse) { *why = "lse is NULL"; return MUON_ERR_INVALID; }
+    muon_status s;
+    if ((s = check_heads(a->q, a->total_q, a->n_heads, a->head_dim, false, "q", &e[0], why)) != MUON_OK) return s;
+    if ((s = check_heads(a->k, a->total_k, a->n_kv_heads, a->head_dim, false, "k", &e[1], why)) != MUON_OK) return s;
+    if ((s = check_heads(a->v, a->total_k, a->n_kv_heads, a->head_dim, false, "v", &e[2], why)) != MUON_OK) return s;
+    if ((s = check_heads(a->out, a->total_q, a->n_heads, a->head_dim, forward, "out", &e[3], why)) != MUON_OK) return s;
+    e[4] = flat(a->lse, (size_t)a->n_heads * a->total_q * 4, forward, "lse");
+    e[5] = flat(a->max_logits, forward && a->max_logits ? (size_t)a->n_heads * 4 : 0, forward, "max_logits");
+    e[6] = flat(a->cu_seqlens_q, a->n_seqs > 0 ? ((size_t)a->n_seqs + 1) * 4 : 0, false, "cu_seqlens_q");
+    e[7] = flat(a->cu_seqlens_k, a->n_seqs > 0 ? ((size_t)a->n_seqs + 1) * 4 : 0, false, "cu_seqlens_k");
+    return MUON_OK;
+}
+
+muon_status check_attention_fwd(const muon_attention_args* a, std::string* why) {
+    Extent e[8];
+    const muon_status s = check_attention(a, true, e, why);
+    return s != MUON_OK ? s : check_extents(e, 8, why);
+}
+
+muon_status check_attention_grad(const muon_attention_grad_args* g, std::string* why) {
+    if (!g) { *why = "args is NULL"; return MUON_ERR_INVALID; }
+    Extent e[13];
+    muon_status s = check_attention(&g->forward, false, e, why);
+    if (s != MUON_OK) return s;
+    const muon_attention_args& a = g->forward;
+    if ((a.total_q > 0 && !g->delta) || !aligned(g->delta, 4)) { *why = "delta is NULL or misaligned"; return MUON_ERR_INVALID; }
+    if ((s = check_heads(g->grad_out, a.total_q, a.n_heads, a.head_dim, false, "grad_out", &e[8], why)) != MUON_OK) return s;
+    if ((s = check_heads(g->dq, a.total_q, a.n_heads, a.head_dim, true, "dq", &e[9], why)) != MUON_OK) return s;
+    if ((s = check_heads(g->dk, a.total_k, a.n_kv_heads, a.head_dim, true, "dk", &e[10], why)) != MUON_OK) return s;
+    if ((s = check_heads(g->dv, a.total_k, a.n_kv_heads, a.head_dim, true, "dv", &e[11], why)) != MUON_OK) return s;
+    e[12] = flat(g->delta, (size_t)a.n_heads * a.total_q * 4, true, "delta");
+    return check_extents(e, 13, why);
+}
+
+HeadView head_view(const muon_heads& v) {
+    return HeadView{static_cast<__nv_bfloat16*>(v.ptr), v.row_stride, v.head_stride};
+}
+
+AttnParams attention_params(const muon_handle* h, const muon_attention_args& a) {
+    AttnParams p{};
+    p.q = head_view(a.q); p.k = head_view(a.k); p.v = head_view(a.v); p.out = head_view(a.out);
+    p.lse = a.lse;
+    p.max_logits = a.max_logits;
+    p.cu_q = a.cu_seqlens_q;
+    p.cu_k = a.cu_seqlens_k;
+    p.n_seqs = a.n_seqs; p.hq = a.n_heads; p.hk = a.n_kv_heads; p.group = a.n_heads / a.n_kv_heads; p.d = a.head_dim;
+    p.total_q = a.total_q; p.total_k = a.total_k;
+    p.scale = a.scale;
+    p.err = h->d_err;
+    return p;
+}
+
+int ckpt_ld(int cols) { return (cols + MUON_CKPT_BLOCK - 1) / MUON_CKPT_BLOCK * MUON_CKPT_BLOCK; }
+
+muon_status check_ckpt(const void* x, int x_dtype, int rows, int cols, long long xs, const int8_t* codes,
+                       const uint8_t* scales, bool store, std::string* why) {
+    if (x_dtype != MUON_BF16 && x_dtype != MUON_FP32) { *why = "bad dtype"; return MUON_ERR_INVALID; }
+    if (rows < 0 || cols <= 0 || cols > (1 << 30)) { *why = "rows must be >= 0 and cols in 1 .. 2^30"; return MUON_ERR_INVALID; }
+    if (rows == 0) return MUON_OK;
+    if (!x || !codes || !scales) { *why = "NULL pointer"; return MUON_ERR_INVALID; }
+    if (rows > 1 && (xs < cols || xs >= (1ll << 38))) { *why = "x_stride must be >= cols"; return MUON_ERR_INVALID; }
+    const size_t b = x_dtype == MUON_BF16 ? 2 : 4, ld = ckpt_ld(cols);
+    if (!aligned(x, b)) { *why = "misaligned x"; return MUON_ERR_INVALID; }
+    if (!aligned(codes, 16)) { *why = "codes must be 16-byte aligned"; return MUON_ERR_INVALID; }
+    Extent e[3] = {flat(x, ((size_t)(rows - 1) * (rows > 1 ? xs : 0) + cols) * b, !store, "x"),
+                   flat(codes, (size_t)rows * ld, store, "codes"),
+                   flat(scales, (size_t)rows * (ld / MUON_CKPT_BLOCK), store, "scales")};
+    return check_extents(e, 3, why);
+}
+
+muon_status check_wgrad_shape(const muon_weight_grad_args* a, std::string* why) {
+    if (!a) { *why = "args is NULL"; return MUON_ERR_INVALID; }
+    if (a->tokens < 0 || a->rows <= 0 || a->cols <= 0) { *why = "tokens must be >= 0, rows and cols > 0"; return MUON_ERR_INVALID; }
+    if ((long long)a->rows * a->cols > (1ll << 31) - 1) { *why = "a matrix may hold at most 2^31-1 elements"; return MUON_ERR_INVALID; }
+    if (a->tokens > (1 << 30)) { *why = "too many tokens"; return MUON_ERR_UNSUPPORTED; }
+    if (a->tokens > 1 && (a->dy_stride < a->rows || a->dy_stride >= (1ll << 38))) { *why = "dy_stride must be >= rows"; return MUON_ERR_INVALID; }
+    return MUON_OK;
+}
+
+size_t wgrad_workspace(const muon_weight_grad_args* a) {
+    (void)a;
+    return 0;
+}
+
+muon_status check_wgrad(const muon_weight_grad_args* a, std::string* why) {
+    muon_status s = check_wgrad_shape(a, why);
+    if (s != MUON_OK) return s;
+    if (a->grad_dtype != MUON_BF16 && a->grad_dtype != MUON_FP32) { *why = "bad grad_dtype"; return MUON_ERR_INVALID; }
+    if (a->accumulate != 0 && a->accumulate != 1) { *why = "accumulate must be 0 or 1"; return MUON_ERR_INVALID; }
+    const size_t b = a->grad_dtype == MUON_BF16 ? 2 : 4, ld = ckpt_ld(a->cols), need = wgrad_workspace(a);
+    if (!a->G || (a->tokens > 0 && (!a->dy || !a->codes || !a->scales))) { *why = "NULL pointer"; return MUON_ERR_INVALID; }
+    if (!aligned(a->G, b) || !aligned(a->dy, 2) || !aligned(a->codes, 16)) { *why = "misaligned pointer"; return MUON_ERR_INVALID; }
+    if (need > 0 && (!a->workspace || a->workspace_bytes < need || !aligned(a->workspace, 16))) {
+        *why = "workspace must hold " + std::to_string(need) + " bytes, 16-byte aligned";
+        return MUON_ERR_INVALID;
+    }
+    const size_t t = a->tokens;
+    Extent e[5] = {flat(a->G, (size_t)a->rows * a->cols * b, true, "G"),
+                   flat(a->dy, t > 0 ? ((t - 1) * (size_t)(t > 1 ? a->dy_stride : 0) + a->rows) * 2 : 0, false, "dy"),
+                   flat(a->codes, t * ld, false, "codes"),
+                   flat(a->scales, t * (ld / MUON_CKPT_BLOCK), false, "scales"),
+                   flat(a->workspace, need, true, "workspace")};
+    return check_extents(e, 5, why);
 }
 
 muon_status ensure_buf(muon_handle* h, DevBuf& b, size_t bytes) {
@@ -1259,6 +1447,128 @@ muon_status muon_qk_clip(muon_handle* h, float* Wq, float* Wk, const float* max_
     return MUON_OK;
 }
 
+muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const float* max_logits, int n_heads,
+                                 int n_kv_heads, int head_dim, int cols, float tau, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    if (!Wq || !Wk || !max_logits) return fail(h, MUON_ERR_INVALID, "Wq, Wk and max_logits are required");
+    if (n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || cols <= 0) return fail(h, MUON_ERR_INVALID, "sizes must be > 0");
+    if (n_heads % n_kv_heads != 0) return fail(h, MUON_ERR_INVALID, "n_heads must be a multiple of n_kv_heads");
+    if ((long long)n_heads * head_dim > (1ll << 29) || (long long)n_heads * head_dim * cols > (1ll << 31) - 1)
+        return fail(h, MUON_ERR_INVALID, "matrix too large");
+    if (!(finite(tau) && tau > 0.f)) return fail(h, MUON_ERR_INVALID, "tau must be finite and > 0");
+    if (!aligned(Wq, 4) || !aligned(Wk, 4) || !aligned(max_logits, 4)) return fail(h, MUON_ERR_INVALID, "misaligned pointer");
+    const Extent e[3] = {flat(Wq, (size_t)n_heads * head_dim * cols * 4, true, "Wq"),
+                         flat(Wk, (size_t)n_kv_heads * head_dim * cols * 4, true, "Wk"),
+                         flat(max_logits, (size_t)n_heads * 4, false, "max_logits")};
+    std::string why;
+    if (check_extents(e, 3, &why) != MUON_OK) return fail(h, MUON_ERR_INVALID, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    CUDA_TRY(h, launch_qk_clip_grouped(Wq, Wk, max_logits, n_heads, n_kv_heads, head_dim, cols, tau, h->num_sms,
+                                       static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
+muon_status muon_validate_attention(const muon_attention_args* args) {
+    std::string why;
+    return check_attention_fwd(args, &why);
+}
+
+muon_status muon_attention(muon_handle* h, const muon_attention_args* a, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    std::string why;
+    const muon_status st = check_attention_fwd(a, &why);
+    if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    NvtxRange nr("attention");
+    CUDA_TRY(h, launch_attention(attention_params(h, *a), static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
+muon_status muon_validate_attention_grad(const muon_attention_grad_args* args) {
+    std::string why;
+    return check_attention_grad(args, &why);
+}
+
+muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_args* g, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    std::string why;
+    const muon_status st = check_attention_grad(g, &why);
+    if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    NvtxRange nr("attention_backward");
+    AttnParams p = attention_params(h, g->forward);
+    p.go = head_view(g->grad_out);
+    p.dq = head_view(g->dq); p.dk = head_view(g->dk); p.dv = head_view(g->dv);
+    p.delta = g->delta;
+    CUDA_TRY(h, launch_attention_backward(p, static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
+muon_status muon_checkpoint_store(muon_handle* h, const void* x, int x_dtype, int rows, int cols, long long x_stride,
+                                  int8_t* codes, uint8_t* scales, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    std::string why;
+    const muon_status st = check_ckpt(x, x_dtype, rows, cols, x_stride, codes, scales, true, &why);
+    if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    if (rows == 0) return MUON_OK;
+    CUDA_TRY(h, launch_checkpoint_store(x, x_dtype == MUON_BF16, rows, cols, rows > 1 ? x_stride : cols, codes, scales,
+                                        h->num_sms, static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
+muon_status muon_checkpoint_load(muon_handle* h, const int8_t* codes, const uint8_t* scales, int rows, int cols,
+                                 void* x, int x_dtype, long long x_stride, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    std::string why;
+    const muon_status st = check_ckpt(x, x_dtype, rows, cols, x_stride, codes, scales, false, &why);
+    if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    if (rows == 0) return MUON_OK;
+    CUDA_TRY(h, launch_checkpoint_load(codes, scales, rows, cols, x, x_dtype == MUON_BF16, rows > 1 ? x_stride : cols,
+                                       h->num_sms, static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
+muon_status muon_weight_grad_workspace(const muon_weight_grad_args* args, size_t* bytes) {
+    std::string why;
+    if (!bytes) return MUON_ERR_INVALID;
+    const muon_status st = check_wgrad_shape(args, &why);
+    if (st == MUON_OK) *bytes = wgrad_workspace(args);
+    return st;
+}
+
+muon_status muon_validate_weight_grad(const muon_weight_grad_args* args) {
+    std::string why;
+    return check_wgrad(args, &why);
+}
+
+muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* a, void* stream) {
+    if (!h) return MUON_ERR_INVALID;
+    std::string why;
+    const muon_status st = check_wgrad(a, &why);
+    if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    DeviceGuard dg(h->device);
+    h->last_error.clear();
+    NvtxRange nr("weight_grad");
+    WgradParams p{};
+    p.dy = static_cast<const __nv_bfloat16*>(a->dy);
+    p.dys = a->tokens > 1 ? a->dy_stride : a->rows;
+    p.codes = a->codes;
+    p.scales = a->scales;
+    p.g = a->G;
+    p.g_bf16 = a->grad_dtype == MUON_BF16;
+    p.accumulate = a->accumulate;
+    p.tokens = a->tokens; p.rows = a->rows; p.cols = a->cols; p.ld = ckpt_ld(a->cols);
+    CUDA_TRY(h, launch_weight_grad(p, static_cast<cudaStream_t>(stream)));
+    return MUON_OK;
+}
+
 muon_status muon_sync(muon_handle* h, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     DeviceGuard dg(h->device);
@@ -1268,6 +1578,9 @@ muon_status muon_sync(muon_handle* h, void* stream) {
     CUDA_TRY(h, cudaMemcpy(&err, h->d_err, sizeof(int), cudaMemcpyDeviceToHost));
     if (err != 0) {
         CUDA_TRY(h, cudaMemset(h->d_err, 0, sizeof(int)));
+        if (err == ERR_SEQLENS)
+            return fail(h, MUON_ERR_INVALID, "an attention call met cu_seqlens out of range (decreasing, negative or "
+                        "above the number of rows): that sequence was passed over");
         return fail(h, MUON_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (code 0x%x)", err);
     }
     return MUON_OK;

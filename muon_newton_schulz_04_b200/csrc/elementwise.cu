@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "kernels.cuh"
+#include "model_ops.cuh"
 #include "ptx.cuh"
 
 #ifndef EW_GROUPS_IN_FLIGHT
@@ -638,7 +639,63 @@ __global__ void __launch_bounds__(EW_THREADS) qk_clip_kernel(float* __restrict__
     }
 }
 
+// Factor of one row of W_q (y = 0) or W_k (y = 1) of QK-Clip with grouped heads: with
+// g_h = min(1, tau / max_logits[h]) a key head's rows take the root of its group's
+// smallest g, a query head's rows g_h divided by that.
+__device__ __forceinline__ float grouped_clip_factor(const float* __restrict__ max_logits, int head, int group,
+                                                     bool key, float tau) {
+    const int base = key ? head * group : head / group * group;
+    float g_min = 1.f, g_own = 1.f;
+    for (int i = 0; i < group; ++i) {
+        const float s = max_logits[base + i];
+        const float g = s > tau ? tau / s : 1.f;
+        g_min = fminf(g_min, g);
+        if (base + i == head) g_own = g;
+    }
+    const float root = sqrtf(g_min);
+    if (key) return root;
+    return root > 0.f ? g_own / root : 0.f;     // an infinite logit gives g = 0
+}
+
+// One warp per row: the factor is found once, and rows that keep their values are not
+// touched.  Bound by memory (8 bytes an element of the clipped rows).
+__global__ void __launch_bounds__(EW_THREADS) qk_clip_grouped_kernel(float* __restrict__ wq, float* __restrict__ wk,
+                                                                    const float* __restrict__ max_logits, int n_heads,
+                                                                    int n_kv_heads, int head_dim, int cols, float tau,
+                                                                    int vec) {
+    pdl_trigger();
+    pdl_wait();
+    const int q_rows = n_heads * head_dim, rows = q_rows + n_kv_heads * head_dim, group = n_heads / n_kv_heads;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (EW_THREADS / 32);
+    for (int r = blockIdx.x * (EW_THREADS / 32) + threadIdx.x / 32; r < rows; r += warps) {
+        const bool key = r >= q_rows;
+        const int row = key ? r - q_rows : r;
+        const float f = grouped_clip_factor(max_logits, row / head_dim, group, key, tau);
+        if (f == 1.0f) continue;
+        float* w = (key ? wk : wq) + (size_t)row * cols;
+        if (vec) {
+            for (int c = lane * 4; c < cols; c += 128) {
+                float4 x = *reinterpret_cast<float4*>(w + c);
+                x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+                *reinterpret_cast<float4*>(w + c) = x;
+            }
+        } else {
+            for (int c = lane; c < cols; c += 32) w[c] *= f;
+        }
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
+                                   int head_dim, int cols, float tau, int num_sms, cudaStream_t s) {
+    const int vec = (cols % 4 == 0) && (reinterpret_cast<uintptr_t>(wq) % 16 == 0) &&
+                    (reinterpret_cast<uintptr_t>(wk) % 16 == 0);
+    const int rows = (n_heads + n_kv_heads) * head_dim;
+    const int blocks = std::min((rows + EW_THREADS / 32 - 1) / (EW_THREADS / 32), num_sms * 8);
+    return launch_pdl(qk_clip_grouped_kernel, dim3(blocks), dim3(EW_THREADS), 0, s, wq, wk, max_logits, n_heads,
+                      n_kv_heads, head_dim, cols, tau, vec);
+}
 
 cudaError_t launch_qk_clip(float* wq, float* wk, const float* max_logits, int n_heads, int head_dim, int cols,
                            float tau, int num_sms, cudaStream_t s) {

@@ -1,0 +1,60 @@
+// model_ops.cuh -- descriptors and launchers of the operators between a layer's
+// forward pass and its Muon step: packed causal attention and its gradients, 8-bit
+// activation checkpoints, and the weight gradient taken from them.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace muon {
+
+// element d of head h of row r: p[r * rs + h * hs + d]
+struct HeadView {
+    __nv_bfloat16* p;
+    long long rs, hs;
+};
+
+struct AttnParams {
+    HeadView q, k, v, out;        // forward operands (out: written by the forward, read by the backward)
+    HeadView go, dq, dk, dv;      // backward only
+    float* lse;                   // [hq][total_q]
+    float* max_logits;            // forward only, may be nullptr
+    float* delta;                 // backward scratch [hq][total_q]: D_i = grad_out_i . O_i
+    const int* cu_q;
+    const int* cu_k;
+    int n_seqs, hq, hk, group, d;
+    int total_q, total_k;
+    float scale;
+    int* err;
+};
+
+// device error word: a sequence whose cu_seqlens are out of range
+constexpr int ERR_SEQLENS = 0x301;
+
+cudaError_t launch_attention(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnParams& p, cudaStream_t s);
+
+constexpr int CKPT_BLOCK = 32;    // values that share a scale byte
+
+cudaError_t launch_checkpoint_store(const void* x, int x_bf16, int rows, int cols, long long xs, int8_t* codes,
+                                    uint8_t* scales, int num_sms, cudaStream_t s);
+cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* scales, int rows, int cols, void* x, int x_bf16,
+                                   long long xs, int num_sms, cudaStream_t s);
+
+struct WgradParams {
+    const __nv_bfloat16* dy;
+    long long dys;
+    const int8_t* codes;
+    const uint8_t* scales;
+    void* g;
+    int g_bf16, accumulate;
+    int tokens, rows, cols, ld;
+};
+cudaError_t launch_weight_grad(const WgradParams& p, cudaStream_t s);
+
+cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
+                                   int head_dim, int cols, float tau, int num_sms, cudaStream_t s);
+
+}  // namespace muon

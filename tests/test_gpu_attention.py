@@ -1,0 +1,341 @@
+"""Packed causal attention with grouped heads, its largest logits and its gradients,
+against the formulas in 64 bits.
+
+Tolerances.  out, dq, dk and dv are rounded to bf16 once (2^-8 of the value at most,
+relative norm below 2^-8), and the exponentials (dS in the backward pass) enter their
+product rounded to bf16, which moves the sum by at most 2^-8 of the sum of its terms'
+magnitudes; for the random-sign terms used here the moved part adds up like the sum
+itself, so the relative norm stays below 2 * 2^-8 = 2^-7.  In the backward pass D_i is
+formed from the rounded out: one more 2^-8 of the same kind, hence 3 * 2^-8.  Where the
+gradients themselves cancel (a query that sees one key has dS = 0), that last part is not
+small beside them: |error of D_i| <= 2^-8 sum_d |do_id out_id| = 2^-8 A_i moves dS_ij by
+P_ij times that, so dq and dk get 2^-8 scale || sum P_ij A_i |k_j| || on top (`slack`).
+lse and the largest logits are fp32 sums of at most 128 + 2^13 terms: 1e-5 absolute for
+logits of order 10 leaves 8 fp32 steps of 2^-20 each.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import muon_newton_schulz_04_b200 as mb
+from muon_newton_schulz_04_b200 import build as mbuild
+
+pytestmark = pytest.mark.gpu
+
+TOL_OUT = 2.0 ** -7
+TOL_GRAD = 3 * 2.0 ** -8
+TOL_STAT = 1e-5
+
+
+@pytest.fixture(scope="module")
+def opt():
+    mbuild.build()
+    o = mb.Muon(mb.config())
+    yield o
+    o.close()
+
+
+def cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def reference(q, k, v, ql, kl, scale, do=None):
+    """out, lse, largest logits (and dq, dk, dv) of the packed rows, in 64 bits by the formulas."""
+    q, k, v = q.double(), k.double(), v.double()
+    hq, hk = q.shape[1], k.shape[1]
+    out, lse, top = torch.zeros_like(q), torch.zeros(hq, q.shape[0], dtype=torch.float64, device=q.device), torch.full(
+        (hq,), -math.inf, dtype=torch.float64, device=q.device)
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    mq, mk = torch.zeros_like(q), torch.zeros_like(k)
+    a = c = 0
+    for lq, lk in zip(ql, kl):
+        see = torch.arange(lk, device=q.device)[None, :] <= torch.arange(lq, device=q.device)[:, None] + lk - lq
+        for h in range(hq):
+            qs, ks, vs = q[a:a + lq, h], k[c:c + lk, h * hk // hq], v[c:c + lk, h * hk // hq]
+            s = scale * qs @ ks.t()
+            s = s.masked_fill(~see, -math.inf)
+            m = s.amax(1, keepdim=True) if lk else s.new_full((lq, 1), -math.inf)
+            e = torch.exp(s - torch.where(torch.isinf(m), 0.0, m))
+            l = e.sum(1, keepdim=True)
+            p = e / torch.where(l == 0, 1.0, l)
+            out[a:a + lq, h] = p @ vs
+            lse[h, a:a + lq] = (torch.where(torch.isinf(m), 0.0, m) + torch.log(l))[:, 0]
+            if lq and lk:
+                top[h] = torch.maximum(top[h], m.max())
+            if do is not None:
+                g = do[a:a + lq, h].double()
+                dp = g @ vs.t()
+                ds = p * (dp - (g * out[a:a + lq, h]).sum(1, keepdim=True))
+                dq[a:a + lq, h] = scale * ds @ ks
+                dk[c:c + lk, h * hk // hq] += scale * ds.t() @ qs
+                dv[c:c + lk, h * hk // hq] += p.t() @ g
+                pa = scale * p * (g * out[a:a + lq, h]).abs().sum(1, keepdim=True)
+                mq[a:a + lq, h] = pa @ ks.abs()
+                mk[c:c + lk, h * hk // hq] += pa.t() @ qs.abs()
+        a, c = a + lq, c + lk
+    return (out, lse, top) if do is None else (out, lse, top, (dq, mq), (dk, mk), (dv, 0 * dv))
+
+
+def close(got, want, tol, what):
+    want, slack = want if isinstance(want, tuple) else (want, 0 * want)
+    got = got.double()
+    assert torch.isfinite(got).all(), what
+    err, most = float((got - want).norm()), tol * float(want.norm()) + 2.0 ** -8 * float(slack.norm())
+    assert err <= most, f"{what}: {err:.3g} > {most:.3g}"
+
+
+def inputs(seed, tq, tk, hq, hk, d):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    return r(tq, hq, d), r(tk, hk, d), r(tk, hk, d), r(tq, hq, d)
+
+
+def run_both(opt, q, k, v, do, cq, ck, scale=None, **kw):
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((q.shape[1], q.shape[0]), 7.0, device="cuda")
+    top = torch.full((q.shape[1],), -math.inf, device="cuda")
+    opt.attention(q, k, v, cq, out=out, lse=lse, max_logits=top, cu_seqlens_k=ck, scale=scale)
+    dq, dk, dv = torch.full_like(q, 7.0), torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    opt.attention_backward(do, q, k, v, out, lse, cq, dq=dq, dk=dk, dv=dv, cu_seqlens_k=ck, scale=scale)
+    opt.sync()
+    return out, lse, top, dq, dk, dv
+
+
+CASES = [
+    # q lengths, k lengths (None: the same), heads, kv heads, head dim
+    ([1], None, 1, 1, 64),
+    ([1, 17, 63, 119], None, 12, 12, 64),
+    ([128, 256, 127, 129, 255, 257], None, 2, 1, 128),
+    ([300, 0, 1, 513], None, 6, 2, 128),
+    ([0, 0, 5, 0], None, 3, 3, 8),
+    ([700], None, 4, 4, 80),
+    ([64, 65], [64, 65], 2, 2, 16),
+    ([40, 1, 200], [300, 77, 200], 4, 1, 64),        # chunks at the end of longer prompts
+    ([200, 130, 3, 9], [60, 129, 0, 300], 4, 2, 128),   # first rows that see nothing; no keys at all
+    ([0, 5], [33, 0], 2, 2, 64),                     # keys without queries, queries without keys
+    ([1500], None, 8, 1, 128),
+    ([1100], [1357], 2, 1, 72),
+    ([3] * 70 + [150], None, 2, 2, 64),              # more sequences than a warp has lanes
+    ([33] * 9, None, 40, 8, 96),
+]
+
+
+@pytest.mark.parametrize("ql,kl,hq,hk,d", CASES)
+def test_forward_and_gradients(opt, ql, kl, hq, hk, d):
+    kl = ql if kl is None else kl
+    q, k, v, do = inputs(sum(ql) + hq * d, sum(ql), sum(kl), hq, hk, d)
+    scale = d ** -0.5
+    out, lse, top, dq, dk, dv = run_both(opt, q, k, v, do, cu(ql), cu(kl))
+    ro, rl, rt, rq, rk, rv = reference(q, k, v, ql, kl, scale, do)
+    close(out, ro, TOL_OUT, "out")
+    empty = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), empty) and bool((out.transpose(0, 1)[empty] == 0).all())
+    assert float((lse.double() - rl)[~empty].abs().max() if (~empty).any() else 0) <= TOL_STAT
+    assert torch.equal(torch.isinf(top), torch.isinf(rt))
+    seen = ~torch.isinf(rt)
+    assert float((top.double() - rt)[seen].abs().max() if seen.any() else 0) <= TOL_STAT
+    close(dq, rq, TOL_GRAD, "dq")
+    close(dk, rk, TOL_GRAD, "dk")
+    close(dv, rv, TOL_GRAD, "dv")
+
+
+def test_gradients_against_differences(opt):
+    """The directional derivative of L = <out, do> in 64-bit differences of the reference forward along a random
+    direction equals <dq, direction> ...: the difference quotient with step 1e-4 is off by O(1e-8), the gradients
+    by TOL_GRAD of the product of norms."""
+    ql = [70, 131]
+    q, k, v, do = inputs(5, 201, 201, 2, 1, 64)
+    _, _, _, dq, dk, dv = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    for x, g, place in ((q, dq, 0), (k, dk, 1), (v, dv, 2)):
+        u = torch.randn(x.shape, generator=gen, device="cuda", dtype=torch.float64)
+        value = []
+        for sign in (1, -1):
+            t = [q.double(), k.double(), v.double()]
+            t[place] = t[place] + sign * 1e-4 * u
+            value.append(float((reference(*t, ql, ql, 64 ** -0.5)[0] * do.double()).sum()))
+        slope = (value[0] - value[1]) / 2e-4
+        assert abs(slope - float((g.double() * u).sum())) <= TOL_GRAD * float(g.double().norm() * u.norm())
+
+
+def test_rows_behind_and_between_sequences_stay(opt):
+    """Rows of no sequence are not written, and what they hold (NaN) reaches nothing."""
+    q, k, v, do = inputs(9, 400, 400, 4, 2, 64)
+    c = torch.tensor([30, 130, 331], dtype=torch.int32, device="cuda")
+    want = [t.clone() for t in run_both(opt, q, k, v, do, c, c)]
+    inside = torch.zeros(400, dtype=torch.bool, device="cuda")
+    inside[30:331] = True
+    for t in (q, k, v, do):
+        t[~inside] = math.nan
+    got = run_both(opt, q, k, v, do, c, c)
+    for name, a, b in zip(("out", "lse", "top", "dq", "dk", "dv"), got, want):
+        assert torch.equal(a, b), name
+    assert bool((got[0][~inside] == 7).all()) and bool((got[1][:, ~inside] == 7).all())
+    for t in got[3:]:
+        assert bool((t[~inside] == 7).all()) and bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_one_sequence_never_reaches_another(opt, bad):
+    ql = [100, 77, 140]
+    q, k, v, do = inputs(10, 317, 317, 2, 2, 128)
+    want = [t.clone() for t in run_both(opt, q, k, v, do, cu(ql), cu(ql))]
+    for t in (q, k, v, do):
+        t[100:177] = bad
+    got = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+    for i in (0, 3, 4, 5):
+        for part in (slice(0, 100), slice(177, 317)):
+            assert torch.equal(got[i][part], want[i][part]), (i, part)
+    assert torch.equal(got[1][:, :100], want[1][:, :100]) and torch.equal(got[1][:, 177:], want[1][:, 177:])
+
+
+def test_views_of_one_fused_projection(opt):
+    """q, k, v (and dq, dk, dv) as strided views of one array, and heads-first arrays: the same bits as dense ones."""
+    ql, hq, hk, d = [150, 3, 260], 6, 2, 64
+    t = sum(ql)
+    q, k, v, do = inputs(11, t, t, hq, hk, d)
+    want = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+    fused = torch.empty(t, hq + 2 * hk, d, dtype=torch.bfloat16, device="cuda")
+    fq, fk, fv = fused[:, :hq], fused[:, hq:hq + hk], fused[:, hq + hk:]
+    fq.copy_(q), fk.copy_(k), fv.copy_(v)
+    grads = torch.zeros_like(fused)
+    hf = lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    out, lse = opt.attention(fq, fk, fv, cu(ql), out=hf(torch.zeros_like(q)))
+    opt.attention_backward(hf(do), fq, fk, fv, out, lse, cu(ql), dq=grads[:, :hq], dk=grads[:, hq:hq + hk],
+                           dv=grads[:, hq + hk:])
+    opt.sync()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(grads, torch.cat(want[3:], 1))
+
+
+def test_max_logits_keep_the_largest(opt):
+    """Micro-batches raise one running maximum; heads whose logits are all negative count too."""
+    q, k, v, _ = inputs(12, 90, 90, 4, 4, 64)
+    k[:, 1] = -q[:, 1].abs()
+    q[:, 1] = q[:, 1].abs()
+    top = torch.full((4,), -math.inf, device="cuda")
+    opt.attention(q, k, v, cu([90]), max_logits=top)
+    first = top.clone()
+    _, _, rt = reference(q, k, v, [90], [90], 64 ** -0.5)
+    assert rt[1] < 0 and float((first.double() - rt).abs().max()) <= TOL_STAT
+    opt.attention((0.5 * q.float()).to(torch.bfloat16), k, v, cu([90]), max_logits=top)
+    opt.sync()
+    keep = torch.maximum(first, 0.5 * first)
+    assert float((top - keep).abs().max()) <= TOL_STAT
+
+
+def test_same_bits_every_time(opt):
+    ql = [513, 40, 300]
+    q, k, v, do = inputs(13, 853, 853, 8, 2, 128)
+    a = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+    b = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_large_logits(opt):
+    """Logits of several hundred: rows are dominated by one key, and nothing overflows."""
+    q, k, v, do = inputs(14, 300, 300, 2, 2, 64)
+    q, k = (q.float() * 8).to(torch.bfloat16), (k.float() * 8).to(torch.bfloat16)
+    out, lse, top, dq, dk, dv = run_both(opt, q, k, v, do, cu([300]), cu([300]))
+    ro, rl, rt, rq, rk, rv = reference(q, k, v, [300], [300], 0.125, do)
+    assert float(rt.max()) > 150
+    close(out, ro, TOL_OUT, "out")
+    # fp32 logits of up to 2^9 carry 2^-15 of rounding each
+    assert float((lse.double() - rl).abs().max()) <= 2.0 ** -13 and float((top.double() - rt).abs().max()) <= 2.0 ** -13
+    close(dv, rv, TOL_GRAD, "dv")
+
+
+def test_captured_calls_replay_on_new_inputs(opt):
+    """Forward and backward captured at the first call, replayed on other inputs and lengths."""
+    q, k, v, do = inputs(15, 260, 260, 4, 2, 64)
+    c = cu([100, 160])
+    out, lse, top = torch.zeros_like(q), torch.zeros(4, 260, device="cuda"), torch.full((4,), -math.inf, device="cuda")
+    grads = [torch.zeros_like(t) for t in (q, k, v)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        opt.attention(q, k, v, c, out=out, lse=lse, max_logits=top)
+        opt.attention_backward(do, q, k, v, out, lse, c, dq=grads[0], dk=grads[1], dv=grads[2])
+    for seed, ql in ((16, [100, 160]), (17, [37, 223]), (18, [1, 259])):
+        for old, new in zip((q, k, v, do), inputs(seed, 260, 260, 4, 2, 64)):
+            old.copy_(new)
+        c.copy_(cu(ql))
+        g.replay()
+        torch.cuda.synchronize()
+        ro, rl, _, rq, rk, rv = reference(q, k, v, ql, ql, 0.125, do)
+        close(out, ro, TOL_OUT, "out")
+        for name, a, b in zip(("dq", "dk", "dv"), grads, (rq, rk, rv)):
+            close(a, b, TOL_GRAD, name)
+    del g
+
+
+def test_two_calls_on_two_streams(opt):
+    a, b = inputs(19, 500, 500, 4, 4, 64), inputs(20, 700, 700, 4, 1, 128)
+    ca, cb = cu([500]), cu([333, 367])
+    want_a, want_b = run_both(opt, *a, ca, ca), run_both(opt, *b, cb, cb)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        oa, la = opt.attention(*a[:3], ca, stream=s1)
+        ob, lb = opt.attention(*b[:3], cb, stream=s2)
+        ga = opt.attention_backward(a[3], *a[:3], oa, la, ca, stream=s1)
+        gb = opt.attention_backward(b[3], *b[:3], ob, lb, cb, stream=s2)
+    torch.cuda.synchronize()
+    for got, want in (((oa, la) + ga, want_a), ((ob, lb) + gb, want_b)):
+        for x, y in zip(got, want[:2] + want[3:]):
+            assert torch.equal(x, y)
+
+
+def test_sequence_bounds_out_of_range_are_reported(opt):
+    """The kernels check cu_seqlens: bad sequences are passed over and muon_sync says so; good ones are computed."""
+    q, k, v, do = inputs(21, 64, 64, 2, 2, 64)
+    for bad in ([0, 20, 65], [0, 30, 20], [-1, 20, 64]):
+        c = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 7.0)
+        opt.attention(q, k, v, c, out=out)
+        with pytest.raises(mb.MuonError) as e:
+            opt.sync()
+        assert e.value.status == mb.MUON_ERR_INVALID
+        opt.sync()
+    assert bool((out[20:] != 7).any())
+
+
+def test_nothing_to_do(opt):
+    e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = opt.attention(e, e, e, cu([]))
+    opt.attention_backward(e, e, e, e, out, lse, cu([0]))
+    opt.sync()
+    assert out.shape == e.shape
+
+
+def test_refusals(opt):
+    q, k, v, do = inputs(22, 16, 16, 4, 2, 64)
+    c = cu([16])
+    out, lse = opt.attention(q, k, v, c)
+    for args, err in (((q.float(), k, v, c), TypeError), ((q, k[:, :, :32], v, c), ValueError),
+                      ((q, k, v[:8], c), ValueError), ((q, k, v, c.long()), ValueError),
+                      ((q, k, v, c.cpu()), ValueError), ((q[:, 0], k, v, c), ValueError)):
+        with pytest.raises(err):
+            opt.attention(*args)
+    with pytest.raises(mb.MuonError) as e:                      # 4 query heads over 3 key heads
+        opt.attention(q, torch.zeros(16, 3, 64, dtype=q.dtype, device="cuda"),
+                      torch.zeros(16, 3, 64, dtype=q.dtype, device="cuda"), c)
+    assert e.value.status == mb.MUON_ERR_INVALID
+    with pytest.raises(mb.MuonError) as e:                      # written over an input
+        opt.attention(q, k, v, c, out=q)
+    assert e.value.status == mb.MUON_ERR_INVALID
+    for d in (60, 136):
+        x = torch.zeros(16, 2, d, dtype=q.dtype, device="cuda")
+        with pytest.raises(mb.MuonError) as e:
+            opt.attention(x, x, x, c)
+        assert e.value.status == mb.MUON_ERR_UNSUPPORTED
+    with pytest.raises(mb.MuonError):
+        opt.attention(q, k, v, c, scale=0.0)
+    with pytest.raises(mb.MuonError):
+        opt.attention_backward(do, q, k, v, out, lse, c, dq=torch.empty_like(q), dk=k)
+    opt.sync()
