@@ -22,8 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_b200.so")
 SOURCES = ["api.cu", "elementwise.cu", "gemm_tc.cu", "gemm_simt.cu", "plan.cpp", "noalloc.cu",
-           "attention.cu", "checkpoint.cu", "weight_grad.cu"]
-HEADERS = ["kernels.cuh", "model_ops.cuh", "ptx.cuh", "plan.h"]
+           "attention.cu", "attention_fwd.cu", "checkpoint.cu", "weight_grad.cu"]
+HEADERS = ["kernels.cuh", "attention.cuh", "model_ops.cuh", "ptx.cuh", "plan.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # extra nvcc flags for experiments with compile-time constants (e.g. -DMUON_S2_STAGES=7)

@@ -551,6 +551,32 @@ muon_status encode_sym_maps(muon_handle* h, CUtensorMap* m2, const void* base, i
                           CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Tensor map of a rows x heads array: dims (head_dim, heads, rows), boxes of 128 rows of
+// 64 columns of one head.  Strides over a single row or head are replaced by ones that
+// the encoder takes; an array without rows gets a map of one row that is never loaded.
+muon_status encode_heads(muon_handle* h, CUtensorMap* m, const muon_heads& v, int rows, int heads, int d,
+                         const void* no_rows) {
+    const void* base = rows > 0 ? v.ptr : no_rows;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)std::max(rows, 1)};
+    const cuuint64_t strides[2] = {heads > 1 && rows > 0 ? (cuuint64_t)v.head_stride * 2 : 16,
+                                   rows > 1 ? (cuuint64_t)v.row_stride * 2 : 16};
+    const cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+    const CUresult r = h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %d rows of %d heads of %d", (int)r, rows, heads, d);
+    return MUON_OK;
+}
+
+muon_status attention_maps(muon_handle* h, const muon_attention_args& a, HeadMaps* m) {
+    muon_status st = load_encoder(h);
+    if (st != MUON_OK) return st;
+    if ((st = encode_heads(h, &m->q, a.q, a.total_q, a.n_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
+    if ((st = encode_heads(h, &m->k, a.k, a.total_k, a.n_kv_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
+    return encode_heads(h, &m->v, a.v, a.total_k, a.n_kv_heads, a.head_dim, h->d_err);
+}
+
 bool is_bf16_path(const muon_handle* h) { return h->cfg.precision == MUON_PREC_BF16; }
 
 // Persistent grid: one CTA (or one two-CTA cluster) per tile, at most one per SM.
@@ -1477,12 +1503,14 @@ muon_status muon_validate_attention(const muon_attention_args* args) {
 muon_status muon_attention(muon_handle* h, const muon_attention_args* a, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     std::string why;
-    const muon_status st = check_attention_fwd(a, &why);
+    muon_status st = check_attention_fwd(a, &why);
     if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
     DeviceGuard dg(h->device);
     h->last_error.clear();
     NvtxRange nr("attention");
-    CUDA_TRY(h, launch_attention(attention_params(h, *a), static_cast<cudaStream_t>(stream)));
+    HeadMaps maps;
+    if ((st = attention_maps(h, *a, &maps)) != MUON_OK) return st;
+    CUDA_TRY(h, launch_attention(attention_params(h, *a), maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }
 

@@ -1,4 +1,4 @@
-// attention.cu -- packed causal attention with grouped heads and its gradients: one
+// attention.cu -- gradients of packed causal attention with grouped heads: one
 // warp per row.  Lanes hold 32 keys (or queries) while logits are formed and head_dim
 // elements while rows are summed.
 #include "model_ops.cuh"
@@ -30,11 +30,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    return v;
-}
-
 __device__ __forceinline__ float dot(const float* a, const __nv_bfloat16* b, int d) {
     float s = 0.f;
     for (int i = 0; i < d; ++i) s = fmaf(a[i], __bfloat162float(b[i]), s);
@@ -43,49 +38,6 @@ __device__ __forceinline__ float dot(const float* a, const __nv_bfloat16* b, int
 
 __device__ __forceinline__ const __nv_bfloat16* at(const HeadView& v, int row, int head) {
     return v.p + row * v.rs + head * v.hs;
-}
-
-__global__ void __launch_bounds__(32 * WARPS) attention_rows(const AttnParams p) {
-    __shared__ float qs[WARPS][DMAX];
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int row = blockIdx.x * WARPS + w, h = blockIdx.y, hk = h / p.group;
-    if (blockIdx.x == 0 && h == 0 && w == 0)
-        for (int i = lane; i < p.n_seqs; i += 32) {     // every sequence is checked once
-            Seq all;
-            load_seq(p, i, all);
-        }
-    if (row >= p.total_q) return;
-    const int s = find_seq(p.cu_q, p.n_seqs, row);
-    Seq sq;
-    if (s < 0 || !load_seq(p, s, sq)) return;
-    for (int i = lane; i < p.d; i += 32) qs[w][i] = __bfloat162float(at(p.q, row, h)[i]);
-    __syncwarp();
-    const int last = min(row - sq.q0 + (sq.k1 - sq.k0) - (sq.q1 - sq.q0), sq.k1 - sq.k0 - 1);
-    float m = -INFINITY, l = 0.f, o[DMAX / 32] = {};
-    for (int j0 = 0; j0 <= last; j0 += 32) {
-        const int j = j0 + lane;
-        const float x = j <= last ? p.scale * dot(qs[w], at(p.k, sq.k0 + j, hk), p.d) : -INFINITY;
-        const float mn = fmaxf(m, warp_max(x)), base = mn == -INFINITY ? 0.f : mn;
-        const float f = expf(m - base), e = j <= last ? expf(x - base) : 0.f;
-        l = l * f + warp_sum(e);
-        m = mn;
-        for (int c = 0; c < DMAX / 32; ++c) o[c] *= f;
-        for (int jj = 0; jj < 32 && j0 + jj <= last; ++jj) {
-            const float pj = __shfl_sync(~0u, e, jj);
-            for (int c = 0; c < DMAX / 32; ++c)
-                if (lane + 32 * c < p.d) o[c] = fmaf(pj, __bfloat162float(at(p.v, sq.k0 + j0 + jj, hk)[lane + 32 * c]), o[c]);
-        }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    for (int c = 0; c < DMAX / 32; ++c)
-        if (lane + 32 * c < p.d) p.out.p[row * p.out.rs + h * p.out.hs + lane + 32 * c] = __float2bfloat16_rn(o[c] * inv);
-    if (lane == 0) {
-        p.lse[(size_t)h * p.total_q + row] = (m == -INFINITY ? 0.f : m) + logf(l);
-        if (p.max_logits != nullptr && m > -INFINITY) {
-            if (m >= 0.f) atomicMax(reinterpret_cast<int*>(p.max_logits + h), __float_as_int(m + 0.f));
-            else atomicMin(reinterpret_cast<unsigned*>(p.max_logits + h), __float_as_uint(m));
-        }
-    }
 }
 
 __global__ void __launch_bounds__(32 * WARPS) attention_dq_rows(const AttnParams p) {
@@ -165,12 +117,6 @@ __global__ void __launch_bounds__(32 * WARPS) attention_dkv_rows(const AttnParam
 }
 
 }  // namespace
-
-cudaError_t launch_attention(const AttnParams& p, cudaStream_t s) {
-    if (p.total_q == 0 || p.n_seqs == 0) return cudaSuccess;
-    attention_rows<<<dim3((p.total_q + WARPS - 1) / WARPS, p.hq), 32 * WARPS, 0, s>>>(p);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attention_backward(const AttnParams& p, cudaStream_t s) {
     if (p.n_seqs == 0) return cudaSuccess;

@@ -1,0 +1,166 @@
+// attention.cuh -- device code shared by the attention kernels: sequence lookup, tensor
+// memory operands and packed arithmetic.
+#pragma once
+
+#include "model_ops.cuh"
+#include "ptx.cuh"
+
+namespace muon {
+
+constexpr int AT_ROWS = 128;                    // rows of a query or key tile = lanes of tensor memory
+constexpr int AT_CHUNK = AT_ROWS * 128;         // bytes of 64 bf16 columns of a tile, one 128-byte swizzle span wide
+constexpr float AT_LOG2E = 1.4426950408889634f;
+
+// One tile of a sequence: rows [q0, q0 + lq) of q, [k0, k0 + lk) of k; `block` counts from
+// 0 over the sequence's `blocks` blocks of rows.
+struct SeqTile {
+    int q0, lq, k0, lk, block, blocks;
+};
+
+// The block with index `t` when the sequences' blocks of `rows` query (or key) rows are
+// counted in order; called by a whole warp, false when t is past the last one.  Sequences
+// whose bounds are out of range count as empty; with check_all every sequence is looked at
+// and a bad one reported.
+__device__ __forceinline__ bool find_tile(const AttnParams& p, bool by_key, int rows, int t, bool check_all, SeqTile& r) {
+    const int lane = (int)(threadIdx.x & 31u);
+    int before = 0;
+    bool found = false;
+    for (int s0 = 0; s0 < p.n_seqs && (!found || check_all); s0 += 32) {
+        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+        if (s0 + lane < p.n_seqs) {
+            q0 = p.cu_q[s0 + lane];
+            q1 = p.cu_q[s0 + lane + 1];
+            k0 = p.cu_k[s0 + lane];
+            k1 = p.cu_k[s0 + lane + 1];
+            if (!(q0 >= 0 && q0 <= q1 && q1 <= p.total_q && k0 >= 0 && k0 <= k1 && k1 <= p.total_k)) {
+                if (check_all) atomicCAS(p.err, 0, ERR_SEQLENS);
+                q0 = q1 = k0 = k1 = 0;
+            }
+        }
+        const int n = ((by_key ? k1 - k0 : q1 - q0) + rows - 1) / rows;
+        int end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + end > t);
+        if (!found && past != 0) {
+            const int l = __ffs((int)past) - 1;
+            r.q0 = __shfl_sync(0xffffffffu, q0, l);
+            r.lq = __shfl_sync(0xffffffffu, q1, l) - r.q0;
+            r.k0 = __shfl_sync(0xffffffffu, k0, l);
+            r.lk = __shfl_sync(0xffffffffu, k1, l) - r.k0;
+            r.blocks = __shfl_sync(0xffffffffu, n, l);
+            r.block = t - (before + __shfl_sync(0xffffffffu, end, l) - r.blocks);
+            found = true;
+        }
+        before += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return found;
+}
+
+__device__ __forceinline__ void spin_ns_at_most(uint64_t ns) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < ns) { }
+}
+
+// ---------------------------------------------------------------- tensor memory
+
+// D[tmem] (+)= A[tmem] * B[smem desc]: A holds one row per lane, two bf16 per column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 lanes x 32 columns: thread i writes r[] to lane (base_lane + i), columns [col, col + 32).
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+        " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- products of tiles
+// Tiles lie in shared memory as 64-column chunks of AT_CHUNK bytes, 128-byte swizzled, one
+// 128-byte line per row.
+
+// D = A * B^T over `dp` columns: A and B 128-row tiles with the contraction along their rows.
+template <int DP>
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS, 0);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t off = (uint32_t)(kk / 4) * AT_CHUNK + (uint32_t)(kk % 4) * 32u;
+        tc_mma_f16(d_tmem, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc, kk != 0);
+    }
+}
+
+// D (+)= A * B: A 128 x 128 bf16 in tensor memory, B a 128-row tile of DP columns.
+template <int DP>
+__device__ __forceinline__ void mma_tb(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
+#pragma unroll
+    for (int kk = 0; kk < AT_ROWS / 16; ++kk)
+        tc_mma_f16_ts(d_tmem, a_tmem + 8 * kk, smem_desc_sw128(b + (uint32_t)kk * 2048u, AT_CHUNK, 1024), idesc,
+                      accumulate || kk != 0);
+}
+
+// Zeroes rows [first, 128) of a tile of DP columns; called by `threads` threads, `t` this one's
+// index.  The caller orders the writes before the products that read the tile.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int t, int threads) {
+    for (int i = first * 8 + t; i < AT_ROWS * 8; i += threads)
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) sts128(tile + (uint32_t)c * AT_CHUNK + (uint32_t)i * 16u, make_uint4(0, 0, 0, 0));
+}
+
+// ---------------------------------------------------------------- arithmetic
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+}  // namespace muon

@@ -33,7 +33,13 @@ struct AttnParams {
 // device error word: a sequence whose cu_seqlens are out of range
 constexpr int ERR_SEQLENS = 0x301;
 
-cudaError_t launch_attention(const AttnParams& p, cudaStream_t s);
+// Tensor maps over [rows][heads][head_dim] arrays, boxes of 128 rows x 64 columns of one
+// head, 128-byte swizzle, zeros outside (go: backward only).
+struct HeadMaps {
+    CUtensorMap q, k, v, go;
+};
+
+cudaError_t launch_attention(const AttnParams& p, const HeadMaps& m, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnParams& p, cudaStream_t s);
 
 constexpr int CKPT_BLOCK = 32;    // values that share a scale byte
