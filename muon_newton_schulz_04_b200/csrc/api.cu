@@ -1522,7 +1522,7 @@ muon_status muon_validate_attention_grad(const muon_attention_grad_args* args) {
 muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_args* g, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     std::string why;
-    const muon_status st = check_attention_grad(g, &why);
+    muon_status st = check_attention_grad(g, &why);
     if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
     DeviceGuard dg(h->device);
     h->last_error.clear();
@@ -1531,7 +1531,10 @@ muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_ar
     p.go = head_view(g->grad_out);
     p.dq = head_view(g->dq); p.dk = head_view(g->dk); p.dv = head_view(g->dv);
     p.delta = g->delta;
-    CUDA_TRY(h, launch_attention_backward(p, static_cast<cudaStream_t>(stream)));
+    HeadMaps maps;
+    if ((st = attention_maps(h, g->forward, &maps)) != MUON_OK) return st;
+    if ((st = encode_heads(h, &maps.go, g->grad_out, p.total_q, p.hq, p.d, h->d_err)) != MUON_OK) return st;
+    CUDA_TRY(h, launch_attention_backward(p, maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }
 

@@ -1,0 +1,615 @@
+// attention_bwd.cu -- gradients of packed causal attention with grouped heads.
+//
+//   P = exp(S - lse),  dP = dO V^T,  dS = P (dP - D),  D_i = dO_i . O_i
+//   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO
+//
+// Two kernels, each owning what it sums, so that nothing is added with atomics and the
+// same inputs give the same bits: the first takes 128 query rows of a head through the
+// keys they see (S, dP, dQ: three products a tile pair), the second 128 key rows of a key
+// head through the queries that see them, for every query head of the group (S^T, dP^T,
+// dV, dK: four).  Forming S and dP twice costs seven products instead of five; in exchange
+// there is no fp32 dQ in memory to add to (for 128-wide heads 64 KiB a tile pair).
+//
+// In both, P and dS go back to tensor memory as bf16 in the place of the fp32 tile that they
+// were formed from, and are the A operand there: only Q, K, V and dO tiles lie in shared
+// memory.  Eight warps form P and dS: warp w owns rows 32 (w % 4) .., warps 0-3 the first 64
+// columns and warps 4-7 the last.
+#include <algorithm>
+
+#include "attention.cuh"
+#include "kernels.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int BW_MATH = 256;
+constexpr int BW_THREADS = BW_MATH + 64;        // + the TMA warp and the MMA warp
+
+constexpr int ERR_BW_LOAD = 0x211, ERR_BW_MMA = 0x212, ERR_BW_MATH = 0x213;
+
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// D = A B: A 128 x 128 bf16 in tensor memory as two halves of 64 columns of the
+// contraction, 64 tensor memory columns apart.
+template <int DP>
+__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
+#pragma unroll
+    for (int kk = 0; kk < AT_ROWS / 16; ++kk)
+        tc_mma_f16_ts(d_tmem, a_tmem + 64u * (kk / 4) + 8u * (kk % 4),
+                      smem_desc_sw128(b + (uint32_t)kk * 2048u, AT_CHUNK, 1024), idesc, accumulate || kk != 0);
+}
+
+// 64 fp32 columns of this thread's row.
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
+    tmem_ld_32x32b_x32(taddr, v[0]);
+    tmem_ld_32x32b_x32(taddr + 32u, v[1]);
+    tmem_ld_wait();
+}
+
+// Writes `n` accumulator columns from `col` of this thread's row, times f, as bf16.
+template <int N>
+__device__ __forceinline__ void store_row(uint32_t taddr, bool any, bool live, float f, int col, int d, __nv_bfloat16* g) {
+#pragma unroll 1
+    for (int i = 0; i < N / 32; ++i) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld_32x32b_x32(taddr + 32u * i, o);
+            tmem_ld_wait();
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = col + 32 * i + 8 * e;
+            if (c < d) {
+                uint32_t v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v[u] = any ? bf16x2(__uint_as_float(o[8 * e + 2 * u]) * f, __uint_as_float(o[8 * e + 2 * u + 1]) * f) : 0u;
+                *reinterpret_cast<uint4*>(g + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+}
+
+// ============================================================================ dQ
+
+template <int DP>
+struct DqLayout {
+    static constexpr int TILE = DP / 64 * AT_CHUNK;
+    static constexpr int KS = DP == 64 ? 4 : 3, VS = DP == 64 ? 3 : 2;      // ring slots: K is used twice
+    static constexpr int BARRIERS = 2 + 2 * KS + 2 * VS + 6;
+    static constexpr int SMEM = 1024 + (2 + KS + VS) * TILE + 8 * BARRIERS + 2 * 128 * 4 + 64;
+    static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;        // S: two buffers of 128
+    static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
+};
+
+struct BwMaps {
+    CUtensorMap q, k, v, go;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(BW_THREADS, 1)
+attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwMaps maps) {
+    using L = DqLayout<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *s_q = smem, *s_do = s_q + L::TILE, *s_k = s_do + L::TILE, *s_v = s_k + L::KS * L::TILE;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_v + L::VS * L::TILE);
+    uint64_t* do_full = q_full + 1;
+    uint64_t *k_full = do_full + 1, *k_empty = k_full + L::KS, *v_full = k_empty + L::KS, *v_empty = v_full + L::VS;
+    uint64_t *s_full = v_empty + L::VS, *dp_full = s_full + 2, *dp_read = dp_full + 1, *ds_ready = dp_read + 1,
+             *dq_full = ds_ready + 1;
+    float* exch = reinterpret_cast<float*>(dq_full + 1);            // [2][128]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(exch + 256);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
+
+    const uint32_t warp = warp_id();
+    const int head = (int)(blockIdx.x % (unsigned)p.hq);
+    pdl_trigger();
+    pdl_wait();
+    if (warp == 0) {
+        SeqTile t;
+        const bool ok = find_tile(p, false, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x == 0, t);
+        if (elect_one()) {
+            *found = ok;
+            info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
+            info[1] = make_int4(ok ? t.blocks - 1 - t.block : 0, 0, 0, 0);      // long rows first
+        }
+    } else if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        mbar_init(q_full, 1);
+        mbar_init(do_full, 1);
+        for (int i = 0; i < L::KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < L::VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
+        mbar_init(&s_full[0], 1);                       // one per buffer: S runs a tile ahead
+        mbar_init(&s_full[1], 1);
+        mbar_init(dp_full, 1);
+        mbar_init(dp_read, BW_MATH);
+        mbar_init(ds_ready, BW_MATH);
+        mbar_init(dq_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (*found) {
+        const int4 sl = info[0];
+        const int q0 = sl.x, lq = sl.y, k0 = sl.z, lk = sl.w;
+        const int row0 = info[1].x * AT_ROWS, shift = lk - lq, kv_head = head / p.group;
+        const int last = min(row0 + AT_ROWS, lq) - 1 + shift;       // last key that any row sees
+        const int n = last < 0 ? 0 : last / AT_ROWS + 1;
+
+        if (warp == 8) {
+            if (elect_one() && n > 0) {
+                mbar_arrive_expect_tx(q_full, L::TILE);
+                for (int c = 0; c < DP / 64; ++c)
+                    tma_load_3d(s_q + c * AT_CHUNK, &maps.q, q_full, 64 * c, head, q0 + row0);
+                bool ok = true;
+                for (int j = 0; j < n + L::KS; ++j) {       // the last turns only wait for the loads to be used
+                    const int ks = j % L::KS, vs = j % L::VS;
+                    if (!mbar_wait(&k_empty[ks], ((uint32_t)(j / L::KS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
+                    if (j < n) {
+                        mbar_arrive_expect_tx(&k_full[ks], L::TILE);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_3d(s_k + ks * L::TILE + c * AT_CHUNK, &maps.k, &k_full[ks], 64 * c, kv_head, k0 + j * AT_ROWS);
+                    }
+                    if (j == 0) {
+                        mbar_arrive_expect_tx(do_full, L::TILE);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_3d(s_do + c * AT_CHUNK, &maps.go, do_full, 64 * c, head, q0 + row0);
+                    }
+                    if (j < n + L::VS &&
+                        !mbar_wait(&v_empty[vs], ((uint32_t)(j / L::VS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
+                    if (j < n) {
+                        mbar_arrive_expect_tx(&v_full[vs], L::TILE);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_3d(s_v + vs * L::TILE + c * AT_CHUNK, &maps.v, &v_full[vs], 64 * c, kv_head, k0 + j * AT_ROWS);
+                    }
+                }
+                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+            }
+        } else if (warp == 9) {
+            if (elect_one() && n > 0) {
+                const uint32_t q_s = smem_u32(s_q), do_s = smem_u32(s_do), k_s = smem_u32(s_k), v_s = smem_u32(s_v);
+                auto wait = [&](uint64_t* b, int use) {
+                    const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_BW_MMA);
+                    tc_fence_after();
+                    return ok;
+                };
+                auto do_s_product = [&](int j) {
+                    mma_abt<DP>(tmem + L::S_COL + 128u * (j & 1), q_s, k_s + (uint32_t)(j % L::KS) * L::TILE);
+                    tc_commit(&s_full[j & 1]);
+                };
+                auto do_dp_product = [&](int j) {
+                    mma_abt<DP>(tmem + L::DP_COL, do_s, v_s + (uint32_t)(j % L::VS) * L::TILE);
+                    tc_commit(dp_full);
+                    tc_commit(&v_empty[j % L::VS]);
+                };
+                bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
+                if (ok) do_s_product(0);
+                ok = ok && wait(do_full, 0) && wait(&v_full[0], 0);
+                if (ok) do_dp_product(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    if (j + 1 < n) {
+                        // its buffer held dS of tile j - 1, whose product runs before
+                        if (!(ok = wait(&k_full[(j + 1) % L::KS], (j + 1) / L::KS))) break;
+                        do_s_product(j + 1);
+                        if (!(ok = wait(dp_read, j) && wait(&v_full[(j + 1) % L::VS], (j + 1) / L::VS))) break;
+                        do_dp_product(j + 1);
+                    }
+                    if (!(ok = wait(ds_ready, j))) break;
+                    mma_halves<DP>(tmem + L::DQ_COL, tmem + L::S_COL + 128u * (j & 1), k_s + (uint32_t)(j % L::KS) * L::TILE, j > 0);
+                    tc_commit(&k_empty[j % L::KS]);
+                }
+                if (ok) tc_commit(dq_full);
+                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+            }
+        } else {
+            const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
+            const uint32_t lane_base = (warp & 3u) * 32u << 16;
+            const int row = row0 + t;
+            const bool live = row < lq;
+            const size_t stat = (size_t)head * p.total_q + q0 + (live ? row : 0);
+            const float c = p.scale * AT_LOG2E;
+            // D of the row: each of its two threads sums one half
+            float dsum = 0.f;
+            if (live) {
+                const long long at_g = (long long)(q0 + row) * p.go.rs + (long long)head * p.go.hs;
+                const long long at_o = (long long)(q0 + row) * p.out.rs + (long long)head * p.out.hs;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const int col = half * (DP / 2) + 8 * i;
+                    if (col < p.d) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(p.go.p + at_g + col);
+                        const uint4 b = *reinterpret_cast<const uint4*>(p.out.p + at_o + col);
+                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            dsum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), dsum);
+                            dsum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), dsum);
+                        }
+                    }
+                }
+            }
+            exch[half * 128 + t] = dsum;
+            math_sync();
+            const float D = exch[t] + exch[128 + t];
+            const float lse2 = live ? p.lse[stat] * AT_LOG2E : 0.f;
+            const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-D, -D);
+            float rest = 0.f;                   // sum of dS: 0 but for the rounding of O in D
+            bool ok = true;
+            for (int j = 0; j < n; ++j) {
+                ok = mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_BW_MATH);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t s_t = tmem + lane_base + L::S_COL + 128u * (j & 1) + 64u * half;
+                uint32_t s[2][32];
+                load64(s_t, s);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    float x, y;
+                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2, l2), x, y);
+                    s[i / 32][i % 32] = __float_as_uint(ex2(x));
+                    s[i / 32][i % 32 + 1] = __float_as_uint(ex2(y));
+                }
+                ok = mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_BW_MATH);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t dp[2][32];
+                load64(tmem + lane_base + L::DP_COL + 64u * half, dp);
+                tc_fence_before();
+                mbar_arrive(dp_read);
+                const int seen = row + shift - j * AT_ROWS - 64 * half;     // column of the last seen key
+                const bool edge = (j + 1) * AT_ROWS > row0 + shift + 1;
+                uint32_t ds[32];
+                uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    uint64_t v = mul2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])),
+                                      add2(pack2(__uint_as_float(dp[i / 32][i % 32]), __uint_as_float(dp[i / 32][i % 32 + 1])), d2));
+                    if (edge) {
+                        float x, y;
+                        unpack2(v, x, y);
+                        v = pack2(i > seen ? 0.f : x, i + 1 > seen ? 0.f : y);
+                    }
+                    sum2 = add2(sum2, v);
+                    float x, y;
+                    unpack2(v, x, y);
+                    ds[i / 2] = bf16x2(x, y);
+                }
+                float a, b;
+                unpack2(sum2, a, b);
+                rest += a + b;
+                tmem_st_32x32b_x32(s_t, ds);
+                if (lk - j * AT_ROWS < AT_ROWS) {
+                    // rows behind the sequence's keys: dS is 0 there, but 0 times what lies behind need not be
+                    zero_rows<DP>(smem_u32(s_k + (j % L::KS) * L::TILE), lk - j * AT_ROWS, (int)threadIdx.x, BW_MATH);
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(ds_ready);
+            }
+            if (ok && n > 0) {
+                ok = mbar_wait(dq_full, 0, abort_flag, p.err, ERR_BW_MATH);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
+            // sum_j P_ij = 1, so D + sum_j dS_ij is sum_j P_ij dP_ij without O's rounding: the
+            // second kernel takes that
+            math_sync();
+            exch[half * 128 + t] = rest;
+            math_sync();
+            if (ok) {
+                if (half == 0 && live) p.delta[stat] = D + exch[t] + exch[128 + t];
+                store_row<DP / 2>(tmem + lane_base + L::DQ_COL + (uint32_t)(half * (DP / 2)), n > 0, live, p.scale,
+                                  half * (DP / 2), p.d,
+                                  p.dq.p + (long long)(q0 + (live ? row : 0)) * p.dq.rs + (long long)head * p.dq.hs);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ============================================================================ dK, dV
+
+template <int DP>
+struct DkvLayout {
+    static constexpr int TILE = DP / 64 * AT_CHUNK;
+    static constexpr int SLOTS = DP == 64 ? 3 : 2;              // of q and of dO
+    static constexpr int BARRIERS = 1 + 4 * SLOTS + 5;
+    static constexpr int SMEM = 1024 + (2 + 2 * SLOTS) * TILE + 8 * BARRIERS + 4 * 128 * 4 + 64;
+    static constexpr uint32_t S_COL = 0, DP_COL = 128, DK_COL = 256, DV_COL = 384;
+    static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
+};
+
+template <int DP>
+__global__ void __launch_bounds__(BW_THREADS, 1)
+attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwMaps maps) {
+    using L = DkvLayout<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *s_k = smem, *s_v = s_k + L::TILE, *s_q = s_v + L::TILE, *s_do = s_q + L::SLOTS * L::TILE;
+    float* stats = reinterpret_cast<float*>(s_do + L::SLOTS * L::TILE);     // two buffers of [lse * log2(e) | D]
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * 128);
+    uint64_t *q_full = kv_full + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
+    uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 1,
+             *dkv_full = ds_ready + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkv_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
+
+    const uint32_t warp = warp_id();
+    const int kv_head = (int)(blockIdx.x % (unsigned)p.hk);
+    pdl_trigger();
+    pdl_wait();
+    if (warp == 0) {
+        SeqTile t;
+        // first blocks of a sequence first: most queries see them
+        const bool ok = find_tile(p, true, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hk), blockIdx.x == 0, t);
+        if (elect_one()) {
+            *found = ok;
+            info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
+            info[1] = make_int4(t.block, 0, 0, 0);
+        }
+    } else if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        mbar_init(kv_full, 1);
+        for (int i = 0; i < L::SLOTS; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&do_full[i], 1);
+            mbar_init(&do_empty[i], 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_ready, BW_MATH);
+        mbar_init(ds_ready, BW_MATH);
+        mbar_init(dkv_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (*found) {
+        const int4 sl = info[0];
+        const int q0 = sl.x, lq = sl.y, k0 = sl.z, lk = sl.w;
+        const int key0 = info[1].x * AT_ROWS, shift = lk - lq;
+        const int tiles = (lq + AT_ROWS - 1) / AT_ROWS, first = max(0, key0 - shift) / AT_ROWS;   // query tiles that see any of the keys
+        const int per_head = max(0, tiles - first), n = per_head * p.group;
+        // item `it`: query tile first + it % per_head of head kv_head * group + it / per_head
+
+        if (warp == 8) {
+            if (elect_one() && n > 0) {
+                mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+                for (int c = 0; c < DP / 64; ++c) {
+                    tma_load_3d(s_k + c * AT_CHUNK, &maps.k, kv_full, 64 * c, kv_head, k0 + key0);
+                    tma_load_3d(s_v + c * AT_CHUNK, &maps.v, kv_full, 64 * c, kv_head, k0 + key0);
+                }
+                bool ok = true;
+                int tile = first, head = kv_head * p.group;
+                for (int it = 0; it < n + L::SLOTS; ++it) {     // the last turns only wait for the loads to be used
+                    const int slot = it % L::SLOTS;
+                    const uint32_t par = ((uint32_t)(it / L::SLOTS) & 1u) ^ 1u;
+                    if (!mbar_wait(&q_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
+                    if (it < n) {
+                        mbar_arrive_expect_tx(&q_full[slot], L::TILE);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_3d(s_q + slot * L::TILE + c * AT_CHUNK, &maps.q, &q_full[slot], 64 * c, head, q0 + tile * AT_ROWS);
+                    }
+                    if (!mbar_wait(&do_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
+                    if (it < n) {
+                        mbar_arrive_expect_tx(&do_full[slot], L::TILE);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_3d(s_do + slot * L::TILE + c * AT_CHUNK, &maps.go, &do_full[slot], 64 * c, head, q0 + tile * AT_ROWS);
+                    }
+                    if (++tile == tiles) { tile = first; ++head; }
+                }
+                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+            }
+        } else if (warp == 9) {
+            if (elect_one() && n > 0) {
+                const uint32_t k_s = smem_u32(s_k), v_s = smem_u32(s_v), q_s = smem_u32(s_q), do_s = smem_u32(s_do);
+                auto wait = [&](uint64_t* b, int use) {
+                    const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_BW_MMA);
+                    tc_fence_after();
+                    return ok;
+                };
+                auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
+                auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
+                bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
+                if (ok) { mma_abt<DP>(tmem + L::S_COL, k_s, q_at(0)); tc_commit(s_full); }
+                ok = ok && wait(&do_full[0], 0);
+                if (ok) { mma_abt<DP>(tmem + L::DP_COL, v_s, do_at(0)); tc_commit(dp_full); }
+                for (int it = 0; it < n && ok; ++it) {
+                    const bool more = it + 1 < n;
+                    if (!(ok = wait(p_ready, it))) break;
+                    mma_halves<DP>(tmem + L::DV_COL, tmem + L::S_COL, do_at(it), it > 0);
+                    tc_commit(&do_empty[it % L::SLOTS]);
+                    if (more) {
+                        // the next S^T takes the place of P^T: products run in order
+                        if (!(ok = wait(&q_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
+                        mma_abt<DP>(tmem + L::S_COL, k_s, q_at(it + 1));
+                        tc_commit(s_full);
+                    }
+                    if (!(ok = wait(ds_ready, it))) break;
+                    mma_halves<DP>(tmem + L::DK_COL, tmem + L::DP_COL, q_at(it), it > 0);
+                    tc_commit(&q_empty[it % L::SLOTS]);
+                    if (more) {
+                        if (!(ok = wait(&do_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
+                        mma_abt<DP>(tmem + L::DP_COL, v_s, do_at(it + 1));
+                        tc_commit(dp_full);
+                    }
+                }
+                if (ok) tc_commit(dkv_full);
+                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+            }
+        } else {
+            const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
+            const uint32_t lane_base = (warp & 3u) * 32u << 16;
+            const int key = key0 + t;
+            const float c = p.scale * AT_LOG2E;
+            const uint64_t c2 = pack2(c, c);
+            const uint32_t s_t = tmem + lane_base + L::S_COL + 64u * half, dp_t = tmem + lane_base + L::DP_COL + 64u * half;
+            bool ok = true;
+            int tile = first, head = kv_head * p.group;
+            // thread t of half 0 fetches lse, of half 1 D, of row t of the next item
+            auto fetch = [&](int tl, int hd) {
+                const int row = tl * AT_ROWS + t;
+                if (row >= lq) return 0.f;
+                const size_t at = (size_t)hd * p.total_q + q0 + row;
+                return half == 0 ? -p.lse[at] * AT_LOG2E : -p.delta[at];
+            };
+            float next = n > 0 ? fetch(tile, head) : 0.f;
+            for (int it = 0; it < n; ++it) {
+                float* st = stats + (it & 1) * 256;
+                st[half * 128 + t] = next;
+                math_sync();
+                const int row0 = tile * AT_ROWS;
+                if (++tile == tiles) { tile = first; ++head; }
+                if (it + 1 < n) next = fetch(tile, head);
+                // query i of the tile sees this thread's key when i >= unseen; rows from lq on are none
+                const int unseen = key - shift - row0 - 64 * half, live = lq - row0 - 64 * half;
+                const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + AT_ROWS > lq;
+                const uint32_t lse_s = smem_u32(st + 64 * half), d_s = smem_u32(st + 128 + 64 * half);
+
+                // a warp whose wait gave up goes on without waiting: the others meet it in math_sync
+                ok = ok && mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                uint32_t s[2][32];
+                load64(s_t, s);
+                uint32_t pr[32];
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                    const uint4 l4 = lds128(lse_s + 4u * i);
+                    float x[4];
+                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2,
+                                 pack2(__uint_as_float(l4.x), __uint_as_float(l4.y))), x[0], x[1]);
+                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32 + 2]), __uint_as_float(s[i / 32][i % 32 + 3])), c2,
+                                 pack2(__uint_as_float(l4.z), __uint_as_float(l4.w))), x[2], x[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = ex2(x[e]);
+                        if (edge && (i + e < unseen || i + e >= live)) x[e] = 0.f;
+                        s[i / 32][i % 32 + e] = __float_as_uint(x[e]);
+                    }
+                    pr[i / 2] = bf16x2(x[0], x[1]);
+                    pr[i / 2 + 1] = bf16x2(x[2], x[3]);
+                }
+                tmem_st_32x32b_x32(s_t, pr);
+                if (row0 + AT_ROWS > lq) {
+                    // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
+                    ok = ok && mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
+                    ok = __all_sync(0xffffffffu, ok);
+                    zero_rows<DP>(smem_u32(s_do + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
+                    zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(p_ready);
+
+                ok = ok && mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                uint32_t dp[2][32];
+                load64(dp_t, dp);
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                    const uint4 d4 = lds128(d_s + 4u * i);
+                    float x[4];
+                    unpack2(mul2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])),
+                                 add2(pack2(__uint_as_float(dp[i / 32][i % 32]), __uint_as_float(dp[i / 32][i % 32 + 1])),
+                                      pack2(__uint_as_float(d4.x), __uint_as_float(d4.y)))), x[0], x[1]);
+                    unpack2(mul2(pack2(__uint_as_float(s[i / 32][i % 32 + 2]), __uint_as_float(s[i / 32][i % 32 + 3])),
+                                 add2(pack2(__uint_as_float(dp[i / 32][i % 32 + 2]), __uint_as_float(dp[i / 32][i % 32 + 3])),
+                                      pack2(__uint_as_float(d4.z), __uint_as_float(d4.w)))), x[2], x[3]);
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i + e < unseen || i + e >= live) x[e] = 0.f;
+                    }
+                    pr[i / 2] = bf16x2(x[0], x[1]);
+                    pr[i / 2 + 1] = bf16x2(x[2], x[3]);
+                }
+                tmem_st_32x32b_x32(dp_t, pr);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(ds_ready);
+            }
+            if (ok && n > 0) {
+                ok = mbar_wait(dkv_full, 0, abort_flag, p.err, ERR_BW_MATH);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
+            if (ok) {
+                const bool mine = key < lk;
+                const long long r = k0 + (mine ? key : 0);
+                const int col = half * (DP / 2);
+                store_row<DP / 2>(tmem + lane_base + L::DK_COL + (uint32_t)col, n > 0, mine, p.scale, col, p.d,
+                                  p.dk.p + r * p.dk.rs + (long long)kv_head * p.dk.hs);
+                store_row<DP / 2>(tmem + lane_base + L::DV_COL + (uint32_t)col, n > 0, mine, 1.f, col, p.d,
+                                  p.dv.p + r * p.dv.rs + (long long)kv_head * p.dv.hs);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Blocks of 128 rows of up to n_seqs sequences: at most one partial block each.
+unsigned most_tiles(int total, int n_seqs) { return (unsigned)(total / AT_ROWS + std::min(n_seqs, total)); }
+
+template <int DP>
+cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) {
+    cudaError_t e;
+    if (p.total_q > 0) {
+        e = cudaFuncSetAttribute(attention_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<DP>::SMEM);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(attention_dq_kernel<DP>, dim3(most_tiles(p.total_q, p.n_seqs) * (unsigned)p.hq), dim3(BW_THREADS),
+                       DqLayout<DP>::SMEM, s, p, maps);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.total_k > 0) {
+        e = cudaFuncSetAttribute(attention_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvLayout<DP>::SMEM);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(attention_dkv_kernel<DP>, dim3(most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk), dim3(BW_THREADS),
+                       DkvLayout<DP>::SMEM, s, p, maps);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_backward(const AttnParams& p, const HeadMaps& m, cudaStream_t s) {
+    if (p.n_seqs == 0) return cudaSuccess;
+    const BwMaps maps{m.q, m.k, m.v, m.go};
+    return p.d <= 64 ? launch_bwd<64>(p, maps, s) : launch_bwd<128>(p, maps, s);
+}
+
+}  // namespace muon

@@ -40,7 +40,7 @@ struct HeadMaps {
 };
 
 cudaError_t launch_attention(const AttnParams& p, const HeadMaps& m, cudaStream_t s);
-cudaError_t launch_attention_backward(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnParams& p, const HeadMaps& m, cudaStream_t s);
 
 constexpr int CKPT_BLOCK = 32;    // values that share a scale byte
 
