@@ -451,9 +451,13 @@ muon_status check_wgrad_shape(const muon_weight_grad_args* a, std::string* why) 
     return MUON_OK;
 }
 
+WgradPlan wgrad_plan(const muon_weight_grad_args* a) {
+    return weight_grad_plan(a->tokens, a->rows, a->cols, aligned(a->dy, 16) && (a->tokens <= 1 || a->dy_stride % 8 == 0));
+}
+
 size_t wgrad_workspace(const muon_weight_grad_args* a) {
-    (void)a;
-    return 0;
+    const WgradPlan w = wgrad_plan(a);
+    return w.dy_bytes + w.partial_bytes;
 }
 
 muon_status check_wgrad(const muon_weight_grad_args* a, std::string* why) {
@@ -575,6 +579,21 @@ muon_status attention_maps(muon_handle* h, const muon_attention_args& a, HeadMap
     if ((st = encode_heads(h, &m->q, a.q, a.total_q, a.n_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
     if ((st = encode_heads(h, &m->k, a.k, a.total_k, a.n_kv_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
     return encode_heads(h, &m->v, a.v, a.total_k, a.n_kv_heads, a.head_dim, h->d_err);
+}
+
+// Tensor map of dy (tokens x rows): boxes of 64 tokens x 64 columns.
+muon_status encode_dy(muon_handle* h, CUtensorMap* m, const WgradParams& p) {
+    muon_status st = load_encoder(h);
+    if (st != MUON_OK) return st;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.rows, (cuuint64_t)p.tokens, 1};
+    const cuuint64_t row = p.tokens > 1 ? (cuuint64_t)p.dys * 2 : (cuuint64_t)align_up((size_t)p.rows * 2, 16);
+    const cuuint64_t strides[2] = {row, row};
+    const cuuint32_t box[3] = {64, 64, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.dy), dims, strides,
+                                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for dy", (int)r);
+    return MUON_OK;
 }
 
 bool is_bf16_path(const muon_handle* h) { return h->cfg.precision == MUON_PREC_BF16; }
@@ -1582,7 +1601,7 @@ muon_status muon_validate_weight_grad(const muon_weight_grad_args* args) {
 muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* a, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     std::string why;
-    const muon_status st = check_wgrad(a, &why);
+    muon_status st = check_wgrad(a, &why);
     if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
     DeviceGuard dg(h->device);
     h->last_error.clear();
@@ -1595,8 +1614,23 @@ muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* a, voi
     p.g = a->G;
     p.g_bf16 = a->grad_dtype == MUON_BF16;
     p.accumulate = a->accumulate;
+    p.vec = aligned(a->G, 16) && a->cols % (p.g_bf16 ? 8 : 4) == 0;
     p.tokens = a->tokens; p.rows = a->rows; p.cols = a->cols; p.ld = ckpt_ld(a->cols);
-    CUDA_TRY(h, launch_weight_grad(p, static_cast<cudaStream_t>(stream)));
+    const WgradPlan w = wgrad_plan(a);
+    p.kblocks = w.kblocks; p.tiles_n = w.tiles_n; p.whole = w.whole; p.rest = w.rest; p.splits = w.splits;
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + w.dy_bytes);
+    p.err = h->d_err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap map{};
+    if (a->tokens > 0) {
+        if (w.dy_bytes > 0) {
+            CUDA_TRY(h, launch_weight_grad_repack(p, w, static_cast<__nv_bfloat16*>(a->workspace), s));
+            p.dy = static_cast<const __nv_bfloat16*>(a->workspace);
+            p.dys = w.dy_ld;
+        }
+        if ((st = encode_dy(h, &map, p)) != MUON_OK) return st;
+    }
+    CUDA_TRY(h, launch_weight_grad(p, map, s));
     return MUON_OK;
 }
 

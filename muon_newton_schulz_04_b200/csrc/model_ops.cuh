@@ -49,16 +49,32 @@ cudaError_t launch_checkpoint_store(const void* x, int x_bf16, int rows, int col
 cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* scales, int rows, int cols, void* x, int x_bf16,
                                    long long xs, int num_sms, cudaStream_t s);
 
+// Split of a weight gradient over the SM pairs, and the workspace that it needs.
+struct WgradPlan {
+    int kblocks;              // blocks of 64 tokens
+    int tiles_n;              // 256-column tiles of G
+    int whole;                // first tiles, computed by one cluster each
+    int rest, splits;         // the others, split along the tokens
+    size_t partial_bytes;     // fp32 partial sums of the split tiles
+    int dy_ld;                // row length of the copy of a dy that TMA cannot read
+    size_t dy_bytes;          // its size, 0: dy is read where it is
+};
+WgradPlan weight_grad_plan(int tokens, int rows, int cols, bool dy_aligned);
+
 struct WgradParams {
     const __nv_bfloat16* dy;
     long long dys;
     const int8_t* codes;
     const uint8_t* scales;
     void* g;
-    int g_bf16, accumulate;
+    int g_bf16, accumulate, vec;
     int tokens, rows, cols, ld;
+    int kblocks, tiles_n, whole, rest, splits;
+    float* partial;
+    int* err;
 };
-cudaError_t launch_weight_grad(const WgradParams& p, cudaStream_t s);
+cudaError_t launch_weight_grad_repack(const WgradParams& p, const WgradPlan& w, __nv_bfloat16* out, cudaStream_t s);
+cudaError_t launch_weight_grad(const WgradParams& p, const CUtensorMap& dy_map, cudaStream_t s);
 
 cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
                                    int head_dim, int cols, float tau, int num_sms, cudaStream_t s);

@@ -1,48 +1,409 @@
-// weight_grad.cu -- G (+)= dy^T x^ with x^ read from an 8-bit checkpoint: one output
-// element per thread, 16 tokens at a time through shared memory.
+// weight_grad.cu -- G (+)= dy^T x^: the gradient of a linear layer's weight, with x^ read
+// from its 8-bit checkpoint.
+//
+// A two-CTA tensor-core GEMM over the tokens: M = rows of G (columns of dy), N = columns of
+// G (of x^), 256 x 256 a tile, 64 tokens a stage.  Both operands have the contraction along
+// their rows in memory, so both are MN-major.  dy arrives by TMA; the codes are turned into
+// bf16 on the way into shared memory by eight warps, a thread 32 codes of one scale:
+// exact, as a code has 7 bits and the unit is a power of two.  So x^ exists in no memory
+// outside the SM, and its traffic is a byte a value.
+//
+// Tiles beyond the last full round over the clusters are split along the tokens so that
+// every cluster has work; their fp32 partial sums go through the caller's workspace and a
+// second kernel adds them in order (no atomics: the same inputs give the same bits).
+#include <algorithm>
+
+#include "kernels.cuh"
 #include "model_ops.cuh"
 #include "ptx.cuh"
 
 namespace muon {
 namespace {
 
-constexpr int T = 16;
+constexpr int WG_TILE = 256;                    // rows and columns of G a tile
+constexpr int WG_BK = 64;                       // tokens a stage
+constexpr int WG_OPERAND = 128 * WG_BK * 2;     // bytes of this CTA's half of an operand
+constexpr int WG_CHUNK = 64 * WG_BK * 2;        // 64 columns of it: 128-byte lines, one per token
+constexpr int WG_STAGES = 6;
+constexpr int WG_CLUSTERS = 74;                 // CTA pairs of a B200
+constexpr int WG_EPI_WARPS = 4, WG_CVT_WARPS = 8;
+constexpr int WG_THREADS = 32 * (WG_EPI_WARPS + WG_CVT_WARPS + 2);
+constexpr int WG_TMA_WARP = WG_EPI_WARPS + WG_CVT_WARPS, WG_MMA_WARP = WG_TMA_WARP + 1;
+constexpr int WG_AHEAD = 4;                     // stages whose codes a thread has in registers
+constexpr int WG_SMEM = 1024 + WG_STAGES * 2 * WG_OPERAND + 8 * (2 * WG_STAGES + 5) + 32;
+constexpr int WG_MIN_BLOCKS = 4;                // fewest 64-token blocks of a split
 
-__device__ __forceinline__ float ckpt_unit(uint32_t e) {
-    // 2^(E - 133): normal from E = 7, a power of two among the subnormals below, NaN at 255
-    return __uint_as_float(e == 255u ? 0x7FC00000u : e >= 7u ? (e - 6u) << 23 : 0x10000u << e);
+constexpr int ERR_WG_LOAD = 0x221, ERR_WG_CVT = 0x222, ERR_WG_MMA = 0x223, ERR_WG_EPI = 0x224;
+
+// bf16 A and B, both MN-major, fp32 accumulation, a 256 x 256 pair tile
+constexpr uint32_t WG_IDESC = idesc_bf16_f32(WG_TILE, WG_TILE, 1) | (1u << 15);
+
+// Work of cluster c: tiles c, c + clusters, ... of the `whole` first ones, then part
+// (c % splits) of tile whole + c / splits.
+struct WgUnit {
+    int tile, k0, k1, slot;     // slot of the partial sum, -1: a whole tile
+};
+
+__device__ __forceinline__ bool unit_of(const WgradParams& p, int c, int i, WgUnit& u) {
+    const int rounds = p.whole / WG_CLUSTERS;
+    if (i < rounds) {
+        u = WgUnit{c + i * WG_CLUSTERS, 0, p.kblocks, -1};
+        return true;
+    }
+    if (i > rounds || c >= p.rest * p.splits) return false;
+    const int part = c % p.splits;
+    u.tile = p.whole + c / p.splits;
+    u.k0 = (int)((long long)p.kblocks * part / p.splits);
+    u.k1 = (int)((long long)p.kblocks * (part + 1) / p.splits);
+    u.slot = p.splits > 1 ? c : -1;
+    return true;
 }
 
-__global__ void __launch_bounds__(T * T) weight_grad_simple(const WgradParams p) {
-    __shared__ float a[T][T + 1], b[T][T + 1];
-    const int tx = threadIdx.x % T, ty = threadIdx.x / T;
-    const int r = blockIdx.y * T + ty, c = blockIdx.x * T + tx;
-    float acc = 0.f;
-    for (int t0 = 0; t0 < p.tokens; t0 += T) {
-        const int t = t0 + ty, rr = blockIdx.y * T + tx;
-        a[ty][tx] = t < p.tokens && rr < p.rows ? __bfloat162float(p.dy[(size_t)t * p.dys + rr]) : 0.f;
-        b[ty][tx] = t < p.tokens && c < p.cols
-                        ? p.codes[(size_t)t * p.ld + c] * ckpt_unit(p.scales[((size_t)t * p.ld + c) / CKPT_BLOCK]) : 0.f;
-        __syncthreads();
-        for (int k = 0; k < T; ++k) acc = fmaf(a[k][ty], b[k][tx], acc);
-        __syncthreads();
+// bf16 bits of 2^(E - 133): subnormal below E = 7, NaN at 255
+__device__ __forceinline__ uint32_t unit_bf16(uint32_t e) {
+    return e == 255u ? 0x7FC0u : e >= 7u ? (e - 6u) << 7 : 1u << e;
+}
+
+// Two codes (the low bytes of the halves of x) times the unit pair.  128 + (c & 127) and
+// 128, or 256 for negative c, are bf16 bit patterns away from the code, and their difference
+// is c.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x, __nv_bfloat162 unit) {
+    const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 v =
+        __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b)), unit);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct Codes {
+    uint4 w[2];
+    uint32_t e;
+};
+
+__device__ __forceinline__ Codes load_codes(const WgradParams& p, int token, int block) {
+    Codes c{{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, 0};
+    if (token < p.tokens && block * CKPT_BLOCK < p.ld) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.codes + (size_t)token * p.ld + (size_t)block * CKPT_BLOCK);
+        c.w[0] = __ldg(src);
+        c.w[1] = __ldg(src + 1);
+        c.e = __ldg(p.scales + (size_t)token * (p.ld / CKPT_BLOCK) + block);
     }
-    if (r >= p.rows || c >= p.cols) return;
-    const size_t o = (size_t)r * p.cols + c;
+    return c;
+}
+
+// Writes a token's 32 values as 64 bytes of its 128-byte line (128-byte swizzle: 16-byte
+// column q of line t lies at q ^ (t & 7)); first: 16-byte column of the first value.
+__device__ __forceinline__ void put_codes(const Codes& c, uint32_t line, int token, int first) {
+    const uint32_t u = unit_bf16(c.e) * 0x10001u;
+    const __nv_bfloat162 unit = *reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {c.w[h].x, c.w[h].y, c.w[h].z, c.w[h].w};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint4 v;
+            v.x = codes_to_bf16(__byte_perm(w[2 * q], 0, 0x4140), unit);
+            v.y = codes_to_bf16(__byte_perm(w[2 * q], 0, 0x4342), unit);
+            v.z = codes_to_bf16(__byte_perm(w[2 * q + 1], 0, 0x4140), unit);
+            v.w = codes_to_bf16(__byte_perm(w[2 * q + 1], 0, 0x4342), unit);
+            sts128(line + (uint32_t)(((first + 2 * h + q) ^ (token & 7)) * 16), v);
+        }
+    }
+}
+
+// 32 finished values of one row of G.
+__device__ __forceinline__ void store_run(const WgradParams& p, int row, int col, const uint32_t (&v)[32]) {
+    const size_t at = (size_t)row * p.cols + col;
     if (p.g_bf16) {
-        __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.g) + o;
-        *g = __float2bfloat16_rn(acc + (p.accumulate ? __bfloat162float(*g) : 0.f));
+        __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.g) + at;
+        if (p.vec && col + 32 <= p.cols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+                uint4 old = make_uint4(0, 0, 0, 0);
+                if (p.accumulate) old = reinterpret_cast<const uint4*>(g)[i];
+                const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(
+                        __uint_as_float(v[8 * i + 2 * e]) + __uint_as_float(o[e] << 16),
+                        __uint_as_float(v[8 * i + 2 * e + 1]) + __uint_as_float(o[e] & 0xFFFF0000u));
+                    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                reinterpret_cast<uint4*>(g)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i < p.cols)
+                    g[i] = __float2bfloat16_rn(__uint_as_float(v[i]) + (p.accumulate ? __bfloat162float(g[i]) : 0.f));
+        }
     } else {
-        float* g = static_cast<float*>(p.g) + o;
-        *g = acc + (p.accumulate ? *g : 0.f);
+        float* g = static_cast<float*>(p.g) + at;
+        if (p.vec && col + 32 <= p.cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.accumulate) old = reinterpret_cast<const float4*>(g)[i];
+                reinterpret_cast<float4*>(g)[i] =
+                    make_float4(__uint_as_float(v[4 * i]) + old.x, __uint_as_float(v[4 * i + 1]) + old.y,
+                                __uint_as_float(v[4 * i + 2]) + old.z, __uint_as_float(v[4 * i + 3]) + old.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i < p.cols) g[i] = __uint_as_float(v[i]) + (p.accumulate ? g[i] : 0.f);
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WG_THREADS, 1)
+weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant__ CUtensorMap dy_map) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + WG_STAGES * WG_OPERAND;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + WG_STAGES * WG_OPERAND);
+    uint64_t* empty = full + WG_STAGES;
+    uint64_t* tfull = empty + WG_STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const uint32_t warp = warp_id();
+    const uint32_t rank = cluster_ctarank();
+    const int cid = (int)cluster_id_x();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < WG_STAGES; ++s) {
+            mbar_init(&full[s], 1 + 2 * WG_CVT_WARPS);  // used in CTA 0: its TMA warp and both CTAs' converting warps
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * WG_EPI_WARPS);    // used in CTA 0
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == WG_MMA_WARP) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+    pdl_wait();
+
+    if (warp == WG_TMA_WARP) {
+        if (elect_one()) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            WgUnit u;
+            for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
+                const int row0 = u.tile / p.tiles_n * WG_TILE + (int)rank * 128;
+                for (int kb = u.k0; kb < u.k1; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, ERR_WG_LOAD)) { ok = false; break; }
+                    const uint32_t full0 = mapa_shared(smem_u32(&full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * WG_OPERAND);
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d_pair(sA + stage * WG_OPERAND + c * WG_CHUNK, &dy_map, full0, row0 + 64 * c, kb * WG_BK, 0);
+                    if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            for (int i = 0; i < WG_STAGES && ok; ++i) {
+                if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, ERR_WG_LOAD)) ok = false;
+                if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok || *abort_flag) {           // let loads in flight land
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 2000000ull) { }
+            }
+        }
+    } else if (warp == WG_MMA_WARP) {
+        if (rank == 0 && elect_one()) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            WgUnit u;
+            for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
+                const uint32_t acc = i & 1;
+                if (!mbar_wait(&tempty[acc], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag, p.err, ERR_WG_MMA)) { ok = false; break; }
+                tc_fence_after();
+                for (int kb = u.k0; kb < u.k1; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, abort_flag, p.err, ERR_WG_MMA)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(sA + stage * WG_OPERAND), b = smem_u32(sB + stage * WG_OPERAND);
+#pragma unroll
+                    for (int kk = 0; kk < WG_BK / 16; ++kk)
+                        tc_mma_f16_pair(tmem + acc * 256u, smem_desc_sw128(a + kk * 2048, WG_CHUNK, 1024),
+                                        smem_desc_sw128(b + kk * 2048, WG_CHUNK, 1024), WG_IDESC, kb != u.k0 || kk != 0);
+                    tc_commit_pair(mapa_shared(smem_u32(&empty[stage]), 0));
+                    tc_commit_pair(mapa_shared(smem_u32(&empty[stage]), 1));
+                    if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                tc_commit_pair(mapa_shared(smem_u32(&tfull[acc]), 0));
+                tc_commit_pair(mapa_shared(smem_u32(&tfull[acc]), 1));
+            }
+            if (!ok || *abort_flag) {
+                tc_commit_pair(mapa_shared(smem_u32(drain), 0));
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 100000000ull) { }
+            }
+        }
+    } else if (warp >= WG_EPI_WARPS) {
+        // converting thread: one token of the stage and one block of 32 of this CTA's 128 columns
+        const int ct = (int)threadIdx.x - 32 * WG_EPI_WARPS, token = ct & 63, blk = ct >> 6;
+        const uint32_t line = smem_u32(sB) + (uint32_t)((blk >> 1) * WG_CHUNK + token * 128);
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        WgUnit u;
+        for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
+            const int block = (u.tile % p.tiles_n * WG_TILE + (int)rank * 128) / CKPT_BLOCK + blk;
+            Codes c[WG_AHEAD];
+#pragma unroll
+            for (int a = 0; a < WG_AHEAD; ++a)
+                if (u.k0 + a < u.k1) c[a] = load_codes(p, (u.k0 + a) * WG_BK + token, block);
+            for (int kb = u.k0; kb < u.k1 && ok; kb += WG_AHEAD) {
+#pragma unroll
+                for (int a = 0; a < WG_AHEAD; ++a) {
+                    if (kb + a >= u.k1) break;
+                    ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, ERR_WG_CVT);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    put_codes(c[a], line + stage * WG_OPERAND, token, (blk & 1) * 4);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if ((threadIdx.x & 31u) == 0) mbar_arrive_remote(mapa_shared(smem_u32(&full[stage]), 0));
+                    if (kb + a + WG_AHEAD < u.k1) c[a] = load_codes(p, (kb + a + WG_AHEAD) * WG_BK + token, block);
+                    if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else {
+        const int lane = (int)(threadIdx.x & 31u);
+        bool ok = true;
+        WgUnit u;
+        for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
+            const uint32_t acc = i & 1;
+            ok = mbar_wait(&tfull[acc], (uint32_t)(i >> 1) & 1u, abort_flag, p.err, ERR_WG_EPI);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            const int in_tile = (int)rank * 128 + (int)warp * 32 + lane;
+            const int row = u.tile / p.tiles_n * WG_TILE + in_tile, col0 = u.tile % p.tiles_n * WG_TILE;
+            const uint32_t t_acc = tmem + acc * 256u + (warp * 32u << 16);
+            float* part = u.slot >= 0 ? p.partial + ((size_t)u.slot * WG_TILE + in_tile) * WG_TILE : nullptr;
+#pragma unroll 1
+            for (int c = 0; c < WG_TILE / 32 && col0 + 32 * c < p.cols; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(t_acc + 32u * c, v);
+                tmem_ld_wait();
+                if (row >= p.rows) continue;
+                if (part != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        reinterpret_cast<uint4*>(part + 32 * c)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                } else {
+                    store_run(p, row, col0 + 32 * c, v);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == WG_MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// Adds the partial sums of the split tiles in order, four columns a thread.
+__global__ void __launch_bounds__(256) weight_grad_join_kernel(const WgradParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int tile = p.whole + (int)blockIdx.y;
+    const int r = (int)blockIdx.x * 4 + (int)threadIdx.x / 64, c = (int)(threadIdx.x & 63u) * 4;
+    const int row = tile / p.tiles_n * WG_TILE + r, col = tile % p.tiles_n * WG_TILE + c;
+    if (row >= p.rows || col >= p.cols) return;
+    const float* src = p.partial + ((size_t)blockIdx.y * p.splits * WG_TILE + r) * WG_TILE + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * WG_TILE * WG_TILE));
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    const size_t at = (size_t)row * p.cols + col;
+    for (int e = 0; e < 4 && col + e < p.cols; ++e) {
+        if (p.g_bf16) {
+            __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.g) + at + e;
+            *g = __float2bfloat16_rn(v[e] + (p.accumulate ? __bfloat162float(*g) : 0.f));
+        } else {
+            float* g = static_cast<float*>(p.g) + at + e;
+            *g = v[e] + (p.accumulate ? *g : 0.f);
+        }
+    }
+}
+
+// dy with rows that TMA cannot read (an odd address or stride), copied to rows of a multiple
+// of 8 elements.
+__global__ void __launch_bounds__(256) weight_grad_repack_kernel(const __nv_bfloat16* __restrict__ dy, long long dys,
+                                                                 int tokens, int rows, int ld,
+                                                                 __nv_bfloat16* __restrict__ out) {
+    pdl_trigger();
+    pdl_wait();
+    for (int t = blockIdx.x; t < tokens; t += gridDim.x)
+        for (int r = threadIdx.x; r < rows; r += 256) out[(size_t)t * ld + r] = dy[(size_t)t * dys + r];
+}
+
+// dy is not read: G = 0, or stays.
+__global__ void __launch_bounds__(256) weight_grad_zero_kernel(const WgradParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const size_t n = (size_t)p.rows * p.cols;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        if (p.g_bf16) static_cast<__nv_bfloat16*>(p.g)[i] = __float2bfloat16_rn(0.f);
+        else static_cast<float*>(p.g)[i] = 0.f;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_weight_grad(const WgradParams& p, cudaStream_t s) {
-    weight_grad_simple<<<dim3((p.cols + T - 1) / T, (p.rows + T - 1) / T), T * T, 0, s>>>(p);
-    return cudaGetLastError();
+WgradPlan weight_grad_plan(int tokens, int rows, int cols, bool dy_aligned) {
+    WgradPlan w{};
+    w.kblocks = (tokens + WG_BK - 1) / WG_BK;
+    w.tiles_n = (cols + WG_TILE - 1) / WG_TILE;
+    const int tiles = (rows + WG_TILE - 1) / WG_TILE * w.tiles_n;
+    w.whole = tiles / WG_CLUSTERS * WG_CLUSTERS;
+    w.rest = tiles - w.whole;
+    w.splits = w.rest == 0 ? 1 : std::max(1, std::min(WG_CLUSTERS / w.rest, w.kblocks / WG_MIN_BLOCKS));
+    w.partial_bytes = w.splits > 1 ? (size_t)w.rest * w.splits * WG_TILE * WG_TILE * sizeof(float) : 0;
+    w.dy_ld = (rows + 7) / 8 * 8;
+    w.dy_bytes = dy_aligned || tokens == 0 ? 0 : ((size_t)tokens * w.dy_ld * 2 + 255) / 256 * 256;
+    return w;
+}
+
+cudaError_t launch_weight_grad_repack(const WgradParams& p, const WgradPlan& w, __nv_bfloat16* out, cudaStream_t s) {
+    return launch_pdl(weight_grad_repack_kernel, dim3(std::min(p.tokens, 16 * 148)), dim3(256), 0, s, p.dy, p.dys, p.tokens,
+                      p.rows, w.dy_ld, out);
+}
+
+cudaError_t launch_weight_grad(const WgradParams& p, const CUtensorMap& dy_map, cudaStream_t s) {
+    if (p.tokens == 0) {
+        if (p.accumulate) return cudaSuccess;
+        const size_t n = (size_t)p.rows * p.cols;
+        return launch_pdl(weight_grad_zero_kernel, dim3((unsigned)std::min<size_t>((n + 255) / 256, 16 * 148)), dim3(256), 0, s, p);
+    }
+    cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM);
+    if (e != cudaSuccess) return e;
+    const int clusters = p.whole > 0 ? WG_CLUSTERS : p.rest * p.splits;
+    e = launch_pdl(weight_grad_kernel, dim3(2 * clusters), dim3(WG_THREADS), WG_SMEM, s, p, dy_map);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_pdl(weight_grad_join_kernel, dim3(WG_TILE / 4, p.rest), dim3(256), 0, s, p);
 }
 
 }  // namespace muon
