@@ -581,18 +581,25 @@ muon_status attention_maps(muon_handle* h, const muon_attention_args& a, HeadMap
     return encode_heads(h, &m->v, a.v, a.total_k, a.n_kv_heads, a.head_dim, h->d_err);
 }
 
-// Tensor map of dy (tokens x rows): boxes of 64 tokens x 64 columns.
-muon_status encode_dy(muon_handle* h, CUtensorMap* m, const WgradParams& p) {
+// Tensor maps of a weight gradient's operands.
+muon_status weight_grad_maps(muon_handle* h, const WgradParams& p, WgradMaps* m) {
     muon_status st = load_encoder(h);
     if (st != MUON_OK) return st;
-    const cuuint64_t dims[3] = {(cuuint64_t)p.rows, (cuuint64_t)p.tokens, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint64_t ddims[3] = {(cuuint64_t)p.rows, (cuuint64_t)p.tokens, 1};
     const cuuint64_t row = p.tokens > 1 ? (cuuint64_t)p.dys * 2 : (cuuint64_t)align_up((size_t)p.rows * 2, 16);
-    const cuuint64_t strides[2] = {row, row};
-    const cuuint32_t box[3] = {64, 64, 1}, estr[3] = {1, 1, 1};
-    const CUresult r = h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.dy), dims, strides,
-                                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dstr[2] = {row, row};
+    const cuuint32_t dbox[3] = {64, 64, 1};
+    CUresult r = h->encode(&m->dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.dy), ddims, dstr,
+                           dbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for dy", (int)r);
+    const cuuint64_t cdims[3] = {(cuuint64_t)p.ld, (cuuint64_t)p.tokens, 1}, cstr[2] = {(cuuint64_t)p.ld, (cuuint64_t)p.ld};
+    const cuuint32_t cbox[3] = {128, 64, 1};
+    r = h->encode(&m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(p.codes), cdims, cstr, cbox, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(h, MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for the codes", (int)r);
     return MUON_OK;
 }
 
@@ -1621,16 +1628,16 @@ muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* a, voi
     p.partial = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + w.dy_bytes);
     p.err = h->d_err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap map{};
+    WgradMaps maps{};
     if (a->tokens > 0) {
         if (w.dy_bytes > 0) {
             CUDA_TRY(h, launch_weight_grad_repack(p, w, static_cast<__nv_bfloat16*>(a->workspace), s));
             p.dy = static_cast<const __nv_bfloat16*>(a->workspace);
             p.dys = w.dy_ld;
         }
-        if ((st = encode_dy(h, &map, p)) != MUON_OK) return st;
+        if ((st = weight_grad_maps(h, p, &maps)) != MUON_OK) return st;
     }
-    CUDA_TRY(h, launch_weight_grad(p, map, s));
+    CUDA_TRY(h, launch_weight_grad(p, maps, s));
     return MUON_OK;
 }
 

@@ -74,7 +74,12 @@ struct WgradParams {
     int* err;
 };
 cudaError_t launch_weight_grad_repack(const WgradParams& p, const WgradPlan& w, __nv_bfloat16* out, cudaStream_t s);
-cudaError_t launch_weight_grad(const WgradParams& p, const CUtensorMap& dy_map, cudaStream_t s);
+// dy (tokens x rows, bf16): boxes of 64 tokens x 64 columns, 128-byte swizzle; the codes
+// (tokens x ld bytes): boxes of 64 tokens x 128 columns.
+struct WgradMaps {
+    CUtensorMap dy, codes;
+};
+cudaError_t launch_weight_grad(const WgradParams& p, const WgradMaps& maps, cudaStream_t s);
 
 cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
                                    int head_dim, int cols, float tau, int num_sms, cudaStream_t s);

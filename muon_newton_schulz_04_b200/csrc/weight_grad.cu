@@ -3,8 +3,8 @@
 //
 // A two-CTA tensor-core GEMM over the tokens: M = rows of G (columns of dy), N = columns of
 // G (of x^), 256 x 256 a tile, 64 tokens a stage.  Both operands have the contraction along
-// their rows in memory, so both are MN-major.  dy arrives by TMA; the codes are turned into
-// bf16 on the way into shared memory by eight warps, a thread 32 codes of one scale:
+// their rows in memory, so both are MN-major.  dy and the codes arrive by TMA; eight warps
+// turn the codes into the bf16 operand in shared memory, a thread 32 codes of one scale:
 // exact, as a code has 7 bits and the unit is a power of two.  So x^ exists in no memory
 // outside the SM, and its traffic is a byte a value.
 //
@@ -24,13 +24,14 @@ constexpr int WG_TILE = 256;                    // rows and columns of G a tile
 constexpr int WG_BK = 64;                       // tokens a stage
 constexpr int WG_OPERAND = 128 * WG_BK * 2;     // bytes of this CTA's half of an operand
 constexpr int WG_CHUNK = 64 * WG_BK * 2;        // 64 columns of it: 128-byte lines, one per token
-constexpr int WG_STAGES = 6;
+constexpr int WG_CODES = 128 * WG_BK;           // bytes of the codes of this CTA's 128 columns
+constexpr int WG_STAGES = 5;
 constexpr int WG_CLUSTERS = 74;                 // CTA pairs of a B200
 constexpr int WG_EPI_WARPS = 4, WG_CVT_WARPS = 8;
 constexpr int WG_THREADS = 32 * (WG_EPI_WARPS + WG_CVT_WARPS + 2);
 constexpr int WG_TMA_WARP = WG_EPI_WARPS + WG_CVT_WARPS, WG_MMA_WARP = WG_TMA_WARP + 1;
-constexpr int WG_AHEAD = 4;                     // stages whose codes a thread has in registers
-constexpr int WG_SMEM = 1024 + WG_STAGES * 2 * WG_OPERAND + 8 * (2 * WG_STAGES + 5) + 32;
+constexpr int WG_GROUP = 8;                     // stages whose scales a thread fetches at once
+constexpr int WG_SMEM = 1024 + WG_STAGES * (2 * WG_OPERAND + WG_CODES) + 8 * (3 * WG_STAGES + 5) + 32;
 constexpr int WG_MIN_BLOCKS = 4;                // fewest 64-token blocks of a split
 
 constexpr int ERR_WG_LOAD = 0x221, ERR_WG_CVT = 0x222, ERR_WG_MMA = 0x223, ERR_WG_EPI = 0x224;
@@ -74,30 +75,27 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x, __nv_bfloat162 uni
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-struct Codes {
-    uint4 w[2];
-    uint32_t e;
-};
-
-__device__ __forceinline__ Codes load_codes(const WgradParams& p, int token, int block) {
-    Codes c{{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, 0};
-    if (token < p.tokens && block * CKPT_BLOCK < p.ld) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.codes + (size_t)token * p.ld + (size_t)block * CKPT_BLOCK);
-        c.w[0] = __ldg(src);
-        c.w[1] = __ldg(src + 1);
-        c.e = __ldg(p.scales + (size_t)token * (p.ld / CKPT_BLOCK) + block);
+// Scale bytes of this thread's (token of the stage, block) for the WG_GROUP stages from kb.
+__device__ __forceinline__ void load_scales(const WgradParams& p, int kb, int k1, int token, int block,
+                                            uint32_t (&e)[WG_GROUP]) {
+#pragma unroll
+    for (int a = 0; a < WG_GROUP; ++a) {
+        const int t = (kb + a) * WG_BK + token;
+        e[a] = kb + a < k1 && t < p.tokens && block * CKPT_BLOCK < p.ld
+                   ? __ldg(p.scales + (size_t)t * (p.ld / CKPT_BLOCK) + block) : 0u;
     }
-    return c;
 }
 
-// Writes a token's 32 values as 64 bytes of its 128-byte line (128-byte swizzle: 16-byte
-// column q of line t lies at q ^ (t & 7)); first: 16-byte column of the first value.
-__device__ __forceinline__ void put_codes(const Codes& c, uint32_t line, int token, int first) {
-    const uint32_t u = unit_bf16(c.e) * 0x10001u;
+// Turns a token's 32 codes at `src` into 64 bytes of its 128-byte line (128-byte swizzle:
+// 16-byte column q of line t lies at q ^ (t & 7)); first: 16-byte column of the first value.
+// Half h ^ swap of the codes is taken in turn h.
+__device__ __forceinline__ void convert_block(uint32_t src, uint32_t line, uint32_t e, int token, int first, int swap) {
+    const uint32_t u = unit_bf16(e) * 0x10001u;
     const __nv_bfloat162 unit = *reinterpret_cast<const __nv_bfloat162*>(&u);
+    const uint4 c[2] = {lds128(src + 16u * swap), lds128(src + 16u * (swap ^ 1))};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {c.w[h].x, c.w[h].y, c.w[h].z, c.w[h].w};
+        const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             uint4 v;
@@ -105,9 +103,17 @@ __device__ __forceinline__ void put_codes(const Codes& c, uint32_t line, int tok
             v.y = codes_to_bf16(__byte_perm(w[2 * q], 0, 0x4342), unit);
             v.z = codes_to_bf16(__byte_perm(w[2 * q + 1], 0, 0x4140), unit);
             v.w = codes_to_bf16(__byte_perm(w[2 * q + 1], 0, 0x4342), unit);
-            sts128(line + (uint32_t)(((first + 2 * h + q) ^ (token & 7)) * 16), v);
+            sts128(line + (uint32_t)(((first + 2 * (h ^ swap) + q) ^ (token & 7)) * 16), v);
         }
     }
+}
+
+// Arrives on a barrier of either CTA of the pair.  What the barrier orders lies in this CTA's
+// own shared memory and is read there by this SM's tensor core, so release at CTA scope is
+// enough, after the proxy fence; at cluster scope every stage would wait for a fence of all
+// memory (8191 tokens into 4096 x 4096: 418 us instead of 
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 
 // 32 finished values of one row of G.
@@ -157,14 +163,16 @@ __device__ __forceinline__ void store_run(const WgradParams& p, int row, int col
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WG_THREADS, 1)
-weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant__ CUtensorMap dy_map) {
+weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant__ WgradMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + WG_STAGES * WG_OPERAND;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + WG_STAGES * WG_OPERAND);
+    uint8_t* sC = sB + WG_STAGES * WG_OPERAND;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sC + WG_STAGES * WG_CODES);
     uint64_t* empty = full + WG_STAGES;
-    uint64_t* tfull = empty + WG_STAGES;
+    uint64_t* raw = empty + WG_STAGES;
+    uint64_t* tfull = raw + WG_STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -176,6 +184,7 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < WG_STAGES; ++s) {
             mbar_init(&full[s], 1 + 2 * WG_CVT_WARPS);  // used in CTA 0: its TMA warp and both CTAs' converting warps
+            mbar_init(&raw[s], 1);                      // this CTA's codes have arrived
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -204,12 +213,15 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
             WgUnit u;
             for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
                 const int row0 = u.tile / p.tiles_n * WG_TILE + (int)rank * 128;
+                const int col0 = u.tile % p.tiles_n * WG_TILE + (int)rank * 128;
                 for (int kb = u.k0; kb < u.k1; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, ERR_WG_LOAD)) { ok = false; break; }
                     const uint32_t full0 = mapa_shared(smem_u32(&full[stage]), 0);
+                    mbar_arrive_expect_tx(&raw[stage], WG_CODES);
+                    tma_load_3d(sC + stage * WG_CODES, &maps.codes, &raw[stage], col0, kb * WG_BK, 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * WG_OPERAND);
                     for (int c = 0; c < 2; ++c)
-                        tma_load_3d_pair(sA + stage * WG_OPERAND + c * WG_CHUNK, &dy_map, full0, row0 + 64 * c, kb * WG_BK, 0);
+                        tma_load_3d_pair(sA + stage * WG_OPERAND + c * WG_CHUNK, &maps.dy, full0, row0 + 64 * c, kb * WG_BK, 0);
                     if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -254,29 +266,34 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
             }
         }
     } else if (warp >= WG_EPI_WARPS) {
-        // converting thread: one token of the stage and one block of 32 of this CTA's 128 columns
-        const int ct = (int)threadIdx.x - 32 * WG_EPI_WARPS, token = ct & 63, blk = ct >> 6;
+        // converting thread: one token of the stage and one block of 32 of this CTA's 128 columns.
+        // The order of the block's halves is such that eight lanes read, and write, all banks.
+        const int ct = (int)threadIdx.x - 32 * WG_EPI_WARPS, token = ct >> 2, blk = ct & 3;
+        const int swap = (blk >> 1) ^ (token & 1);
         const uint32_t line = smem_u32(sB) + (uint32_t)((blk >> 1) * WG_CHUNK + token * 128);
+        const uint32_t src = smem_u32(sC) + (uint32_t)(token * 128 + blk * 32);
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         WgUnit u;
         for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
             const int block = (u.tile % p.tiles_n * WG_TILE + (int)rank * 128) / CKPT_BLOCK + blk;
-            Codes c[WG_AHEAD];
+            uint32_t next[WG_GROUP];
+            load_scales(p, u.k0, u.k1, token, block, next);
+            for (int kb = u.k0; kb < u.k1 && ok; kb += WG_GROUP) {
+                uint32_t e[WG_GROUP];
 #pragma unroll
-            for (int a = 0; a < WG_AHEAD; ++a)
-                if (u.k0 + a < u.k1) c[a] = load_codes(p, (u.k0 + a) * WG_BK + token, block);
-            for (int kb = u.k0; kb < u.k1 && ok; kb += WG_AHEAD) {
+                for (int a = 0; a < WG_GROUP; ++a) e[a] = next[a];
+                load_scales(p, kb + WG_GROUP, u.k1, token, block, next);
 #pragma unroll
-                for (int a = 0; a < WG_AHEAD; ++a) {
+                for (int a = 0; a < WG_GROUP; ++a) {
                     if (kb + a >= u.k1) break;
-                    ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, ERR_WG_CVT);
+                    // the stage's operand is free, too: its codes were asked for after that
+                    ok = mbar_wait(&raw[stage], phase, abort_flag, p.err, ERR_WG_CVT);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    put_codes(c[a], line + stage * WG_OPERAND, token, (blk & 1) * 4);
+                    convert_block(src + stage * WG_CODES, line + stage * WG_OPERAND, e[a], token, (blk & 1) * 4, swap);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if ((threadIdx.x & 31u) == 0) mbar_arrive_remote(mapa_shared(smem_u32(&full[stage]), 0));
-                    if (kb + a + WG_AHEAD < u.k1) c[a] = load_codes(p, (kb + a + WG_AHEAD) * WG_BK + token, block);
+                    if ((threadIdx.x & 31u) == 0) arrive_pair(mapa_shared(smem_u32(&full[stage]), 0));
                     if (++stage == WG_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -392,7 +409,7 @@ cudaError_t launch_weight_grad_repack(const WgradParams& p, const WgradPlan& w, 
                       p.rows, w.dy_ld, out);
 }
 
-cudaError_t launch_weight_grad(const WgradParams& p, const CUtensorMap& dy_map, cudaStream_t s) {
+cudaError_t launch_weight_grad(const WgradParams& p, const WgradMaps& maps, cudaStream_t s) {
     if (p.tokens == 0) {
         if (p.accumulate) return cudaSuccess;
         const size_t n = (size_t)p.rows * p.cols;
@@ -401,7 +418,7 @@ cudaError_t launch_weight_grad(const WgradParams& p, const CUtensorMap& dy_map, 
     cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM);
     if (e != cudaSuccess) return e;
     const int clusters = p.whole > 0 ? WG_CLUSTERS : p.rest * p.splits;
-    e = launch_pdl(weight_grad_kernel, dim3(2 * clusters), dim3(WG_THREADS), WG_SMEM, s, p, dy_map);
+    e = launch_pdl(weight_grad_kernel, dim3(2 * clusters), dim3(WG_THREADS), WG_SMEM, s, p, maps);
     if (e != cudaSuccess || p.splits == 1) return e;
     return launch_pdl(weight_grad_join_kernel, dim3(WG_TILE / 4, p.rest), dim3(256), 0, s, p);
 }
