@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 from typing import List, Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -90,7 +91,16 @@ class _WeightGradArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+# the two attention structures as one pack call each (a third of the time of filling the
+# ctypes structures field by field)
+_ATTENTION_PACK = struct.Struct("@6i2Pf" + "P2q" * 4 + "2P")
+_ATTENTION_GRAD_PACK = struct.Struct("@6i2Pf" + "P2q" * 4 + "2P" + "P2q" * 4 + "P")
+assert (_ATTENTION_PACK.size, _ATTENTION_GRAD_PACK.size) == (ctypes.sizeof(_AttentionArgs),
+                                                             ctypes.sizeof(_AttentionGradArgs))
+
 _LIB: Optional[ctypes.CDLL] = None
+_raw_stream = None
+torch = None        # imported by the first handle: building the library and planning need no torch
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -192,6 +202,13 @@ class Group:
     scale: float = 1.0
 
 
+def _import_torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+
+
 CKPT_BLOCK = 32     # values of an 8-bit checkpoint that share a scale
 
 
@@ -205,7 +222,7 @@ class Checkpoint:
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "Checkpoint":
-        import torch
+        _import_torch()
         blocks = -(-cols // CKPT_BLOCK)
         return Checkpoint(torch.empty(rows, blocks * CKPT_BLOCK, dtype=torch.int8, device=device),
                           torch.empty(rows, blocks, dtype=torch.uint8, device=device), cols)
@@ -216,31 +233,44 @@ class Checkpoint:
 
 
 def _check_checkpoint(ckpt: Checkpoint, device: int):
-    import torch
+    rows, cols = ckpt.codes.shape
     blocks = -(-ckpt.cols // CKPT_BLOCK)
-    _check_tensors([ckpt.codes], (ckpt.rows, blocks * CKPT_BLOCK), True, torch.int8, device)
-    _check_tensors([ckpt.scales], (ckpt.rows, blocks), True, torch.uint8, device)
+    if cols != blocks * CKPT_BLOCK or tuple(ckpt.scales.shape) != (rows, blocks):
+        raise ValueError(f"a checkpoint of {rows} x {ckpt.cols} values has codes [{rows}, {blocks * CKPT_BLOCK}] and "
+                         f"scales [{rows}, {blocks}], got {tuple(ckpt.codes.shape)} and {tuple(ckpt.scales.shape)}")
+    if ckpt.codes.dtype != torch.int8 or ckpt.scales.dtype != torch.uint8:
+        raise ValueError("expected int8 codes and uint8 scales")
+    _check_dense("codes", ckpt.codes, device)
+    _check_dense("scales", ckpt.scales, device)
 
 
-def _check_heads(name: str, t, shape, device: int):
-    """A bf16 CUDA tensor [rows, heads, head_dim] of the given shape with a dense last dimension."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected torch.bfloat16")
-    if not t.is_cuda or t.device.index != device:
+def _check_dense(name: str, t, device: int):
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
-    if tuple(t.shape) != tuple(shape):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _heads(name: str, t, shape, device: int):
+    """(address, row stride, head stride) of a bf16 CUDA tensor [rows, heads, head_dim] of the given shape with a
+    dense last dimension."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected torch.bfloat16")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    rows, heads, last = t.stride()
+    if last != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), rows, heads
 
 
 def _check_rows(name: str, t, device: int):
     """A 2-D CUDA tensor with dense rows; returns its row stride."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be 2-D with dense rows")
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
     return t.stride(0)
 
@@ -279,27 +309,35 @@ def _check_tensors(ts, shape, on_cuda: bool, dtype=None, device: Optional[int] =
 def _stream(stream, device: Optional[int] = None) -> int:
     """The raw cudaStream_t: the given stream, else the current stream of `device`
     (of the current device when None)."""
-    import torch
+    global _raw_stream
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        if _raw_stream is not None and device is not None:
+            return _raw_stream(device)
+        _import_torch()
+        raw = torch.cuda.current_stream(device).cuda_stream
+        # from now on (CUDA is initialised) what that asks, without the stream object: 1 us less a call
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _on_stream(stream, device: int):
-    """Context in which torch allocates for work on `stream` (a torch stream, a raw cudaStream_t or None)."""
-    import contextlib
-    import torch
+def _empty(shape, dtype, like, stream):
+    """A new tensor on the device of `like` for work on `stream` (a torch stream, a raw cudaStream_t or None for the
+    current one): the caching allocator reuses memory in the order of the stream that it was allocated on."""
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
+        stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                  else torch.cuda.default_stream(like.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 class Muon:
     """A handle of the C library bound to one CUDA device."""
 
     def __init__(self, cfg: Optional[MuonConfig] = None, device: int = 0):
+        _import_torch()
         self._h = ctypes.c_void_p()
         self.cfg = cfg if cfg is not None else config()
         st = lib().muon_create(ctypes.byref(self.cfg), int(device), ctypes.byref(self._h))
@@ -453,7 +491,6 @@ class Muon:
     def qk_clip_grouped(self, Wq, Wk, max_logits, head_dim: int, tau: float, stream=None):
         """QK-Clip of a layer whose query heads share key heads (see muon_qk_clip_grouped): Wq fp32
         (n_heads * head_dim) x cols, Wk fp32 (n_kv_heads * head_dim) x cols, max_logits as `attention` leaves it."""
-        import torch
         for name, t in (("Wq", Wq), ("Wk", Wk), ("max_logits", max_logits)):
             if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
@@ -468,29 +505,31 @@ class Muon:
                                                Wk.shape[0] // head_dim, head_dim, Wq.shape[1], float(tau),
                                                ctypes.c_void_p(_stream(stream, self.device))), "muon_qk_clip_grouped")
 
-    def _attention_args(self, q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits):
-        import torch
+    def _attention_fields(self, q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits):
+        """The fields of _AttentionArgs in order."""
         if q.dim() != 3 or k.dim() != 3:
             raise ValueError("q and k must be [rows, heads, head_dim]")
         (tq, hq, d), (tk, hk, _) = q.shape, k.shape
+        dev = self.device
         cu_k = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
         for name, t in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_k)):
-            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or not t.is_cuda:
+            if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() < 1:
                 raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
-            if t.device.index != self.device:
-                raise ValueError(f"{name} is on {t.device}, the handle on cuda:{self.device}")
-            if t.numel() != cu_seqlens.numel() or t.numel() < 1:
-                raise ValueError("cu_seqlens and cu_seqlens_k must hold one entry more than there are sequences")
-        _check_tensors([lse], (hq, tq), True, torch.float32, self.device)
+            _check_dense(name, t, dev)
+        n = cu_seqlens.numel()
+        if cu_k.numel() != n:
+            raise ValueError("cu_seqlens and cu_seqlens_k must hold one entry more than there are sequences")
+        if lse.dtype is not torch.float32 or lse.shape != (hq, tq):
+            raise ValueError(f"lse must be float32 of shape {(hq, tq)}")
+        _check_dense("lse", lse, dev)
         if max_logits is not None:
-            _check_tensors([max_logits], (hq,), True, torch.float32, self.device)
-        return _AttentionArgs(cu_seqlens.numel() - 1, hq, hk, d, tq, tk, cu_seqlens.data_ptr(), cu_k.data_ptr(),
-                              d ** -0.5 if scale is None else float(scale),
-                              _check_heads("q", q, (tq, hq, d), self.device),
-                              _check_heads("k", k, (tk, hk, d), self.device),
-                              _check_heads("v", v, (tk, hk, d), self.device),
-                              _check_heads("out", out, (tq, hq, d), self.device), lse.data_ptr(),
-                              None if max_logits is None else max_logits.data_ptr())
+            if max_logits.dtype is not torch.float32 or max_logits.shape != (hq,):
+                raise ValueError(f"max_logits must be float32 of shape {(hq,)}")
+            _check_dense("max_logits", max_logits, dev)
+        kv = (tk, hk, d)
+        return (n - 1, hq, hk, d, tq, tk, cu_seqlens.data_ptr(), cu_k.data_ptr(), d ** -0.5 if scale is None else scale,
+                *_heads("q", q, q.shape, dev), *_heads("k", k, kv, dev), *_heads("v", v, kv, dev),
+                *_heads("out", out, q.shape, dev), lse.data_ptr(), 0 if max_logits is None else max_logits.data_ptr())
 
     def attention(self, q, k, v, cu_seqlens, out=None, lse=None, max_logits=None, scale: Optional[float] = None,
                   cu_seqlens_k=None, stream=None):
@@ -499,90 +538,85 @@ class Muon:
         keys are packed otherwise), scale 1 / sqrt(head_dim) by default.  Writes out (layout of q), lse
         [heads, rows] fp32 and raises max_logits [heads] fp32 to the largest logit of each head, for qk_clip.
         Returns (out, lse); buffers that are not given are allocated, rows of no sequence left as they are."""
-        import torch
-        with torch.cuda.device(self.device), _on_stream(stream, self.device):
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if lse is None:
-                lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-        args = self._attention_args(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits)
-        self._check(lib().muon_attention(self._h, ctypes.byref(args), ctypes.c_void_p(_stream(stream, self.device))),
-                    "muon_attention")
+        if out is None:
+            out = _empty(q.shape, q.dtype, q, stream)
+        if lse is None:
+            lse = _empty((q.shape[1], q.shape[0]) if q.dim() == 3 else (0,), torch.float32, q, stream)
+        args = _AttentionArgs.from_buffer_copy(_ATTENTION_PACK.pack(
+            *self._attention_fields(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits)))
+        self._check(lib().muon_attention(self._h, args, _stream(stream, self.device)), "muon_attention")
         return out, lse
 
     def attention_backward(self, grad_out, q, k, v, out, lse, cu_seqlens, dq=None, dk=None, dv=None,
                            scale: Optional[float] = None, cu_seqlens_k=None, stream=None):
         """Gradients of `attention` (see muon_attention_backward) from its inputs, out and lse.  Returns
         (dq, dk, dv); buffers that are not given are allocated, rows of no sequence left as they are."""
-        import torch
-        with torch.cuda.device(self.device), _on_stream(stream, self.device):
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-            delta = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-        fwd = self._attention_args(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, None)
-        args = _AttentionGradArgs(fwd, _check_heads("grad_out", grad_out, q.shape, self.device),
-                                  _check_heads("dq", dq, q.shape, self.device),
-                                  _check_heads("dk", dk, k.shape, self.device),
-                                  _check_heads("dv", dv, k.shape, self.device), delta.data_ptr())
-        self._check(lib().muon_attention_backward(self._h, ctypes.byref(args),
-                                                  ctypes.c_void_p(_stream(stream, self.device))),
+        fields = self._attention_fields(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, None)
+        dq = _empty(q.shape, q.dtype, q, stream) if dq is None else dq
+        dk = _empty(k.shape, k.dtype, k, stream) if dk is None else dk
+        dv = _empty(v.shape, v.dtype, v, stream) if dv is None else dv
+        delta = _empty(lse.shape, torch.float32, q, stream)
+        dev = self.device
+        args = _AttentionGradArgs.from_buffer_copy(_ATTENTION_GRAD_PACK.pack(
+            *fields, *_heads("grad_out", grad_out, q.shape, dev), *_heads("dq", dq, q.shape, dev),
+            *_heads("dk", dk, k.shape, dev), *_heads("dv", dv, v.shape, dev), delta.data_ptr()))
+        self._check(lib().muon_attention_backward(self._h, args, _stream(stream, self.device)),
                     "muon_attention_backward")
         return dq, dk, dv
 
     def checkpoint(self, x, ckpt: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
         """x (2-D, bf16 or fp32, dense rows) in 8 bits, for the backward pass (see muon_checkpoint_store)."""
-        import torch
         stride = _check_rows("x", x, self.device)
+        code = _dtype_code(x)
+        rows, cols = x.shape
         if ckpt is None:
-            with torch.cuda.device(self.device), _on_stream(stream, self.device):
-                ckpt = Checkpoint.empty(x.shape[0], x.shape[1], x.device)
-        _check_checkpoint(ckpt, self.device)
-        if (ckpt.rows, ckpt.cols) != tuple(x.shape):
-            raise ValueError(f"the checkpoint holds {ckpt.rows} x {ckpt.cols} values, x is {tuple(x.shape)}")
-        self._check(lib().muon_checkpoint_store(self._h, x.data_ptr(), _dtype_code(x), x.shape[0], x.shape[1], stride,
-                                                ckpt.codes.data_ptr(), ckpt.scales.data_ptr(),
-                                                ctypes.c_void_p(_stream(stream, self.device))),
+            blocks = -(-cols // CKPT_BLOCK)
+            ckpt = Checkpoint(_empty((rows, blocks * CKPT_BLOCK), torch.int8, x, stream),
+                              _empty((rows, blocks), torch.uint8, x, stream), cols)
+        else:
+            _check_checkpoint(ckpt, self.device)
+            if (ckpt.rows, ckpt.cols) != (rows, cols):
+                raise ValueError(f"the checkpoint holds {ckpt.rows} x {ckpt.cols} values, x is {rows} x {cols}")
+        self._check(lib().muon_checkpoint_store(self._h, x.data_ptr(), code, rows, cols, stride, ckpt.codes.data_ptr(),
+                                                ckpt.scales.data_ptr(), _stream(stream, self.device)),
                     "muon_checkpoint_store")
         return ckpt
 
     def checkpoint_load(self, ckpt: Checkpoint, out=None, stream=None):
         """The values of a checkpoint, written to `out` (bf16 or fp32, dense rows; bf16 when not given)."""
-        import torch
         _check_checkpoint(ckpt, self.device)
+        rows, cols = ckpt.rows, ckpt.cols
         if out is None:
-            with torch.cuda.device(self.device), _on_stream(stream, self.device):
-                out = torch.empty(ckpt.rows, ckpt.cols, dtype=torch.bfloat16, device=ckpt.codes.device)
+            out = _empty((rows, cols), torch.bfloat16, ckpt.codes, stream)
         stride = _check_rows("out", out, self.device)
-        if tuple(out.shape) != (ckpt.rows, ckpt.cols):
-            raise ValueError(f"the checkpoint holds {ckpt.rows} x {ckpt.cols} values, out is {tuple(out.shape)}")
-        self._check(lib().muon_checkpoint_load(self._h, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ckpt.rows,
-                                               ckpt.cols, out.data_ptr(), _dtype_code(out), stride,
-                                               ctypes.c_void_p(_stream(stream, self.device))), "muon_checkpoint_load")
+        if tuple(out.shape) != (rows, cols):
+            raise ValueError(f"the checkpoint holds {rows} x {cols} values, out is {tuple(out.shape)}")
+        self._check(lib().muon_checkpoint_load(self._h, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), rows, cols,
+                                               out.data_ptr(), _dtype_code(out), stride, _stream(stream, self.device)),
+                    "muon_checkpoint_load")
         return out
 
     def weight_grad(self, dy, ckpt: Checkpoint, G, accumulate: bool = False, stream=None):
         """G = dy^T x^ (or G += with `accumulate`): the gradient of the weight of y = x W^T from the checkpoint of x
         (see muon_weight_grad).  dy bf16 [tokens, rows] with dense rows; G fp32 or bf16 [rows, cols], the gradient
         that `step` takes.  Returns G."""
-        import torch
         _check_checkpoint(ckpt, self.device)
         stride = _check_rows("dy", dy, self.device)
-        if dy.dtype != torch.bfloat16:
+        if dy.dtype is not torch.bfloat16:
             raise TypeError(f"dy: unsupported dtype {dy.dtype}, expected torch.bfloat16")
-        if dy.shape[0] != ckpt.rows:
-            raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {ckpt.rows}")
-        _check_tensors([G], (dy.shape[1], ckpt.cols), True, None, self.device)
-        args = _WeightGradArgs(dy.shape[0], dy.shape[1], ckpt.cols, dy.data_ptr(), stride, ckpt.codes.data_ptr(),
-                               ckpt.scales.data_ptr(), G.data_ptr(), _dtype_code(G), int(accumulate), None, 0)
+        tokens, rows = dy.shape
+        if tokens != ckpt.rows:
+            raise ValueError(f"dy has {tokens} rows, the checkpoint {ckpt.rows}")
+        if tuple(G.shape) != (rows, ckpt.cols):
+            raise ValueError(f"G must be {rows} x {ckpt.cols}, got {tuple(G.shape)}")
+        _check_dense("G", G, self.device)
+        args = _WeightGradArgs(tokens, rows, ckpt.cols, dy.data_ptr(), stride, ckpt.codes.data_ptr(),
+                               ckpt.scales.data_ptr(), G.data_ptr(), _dtype_code(G), 1 if accumulate else 0, None, 0)
         need = ctypes.c_size_t(0)
-        st = lib().muon_weight_grad_workspace(ctypes.byref(args), ctypes.byref(need))
-        if st == MUON_OK and need.value:
-            with torch.cuda.device(self.device), _on_stream(stream, self.device):
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=G.device)
+        if lib().muon_weight_grad_workspace(args, need) == MUON_OK and need.value:
+            workspace = _empty((need.value,), torch.uint8, G, stream)
             args.workspace, args.workspace_bytes = workspace.data_ptr(), need.value
-        self._check(lib().muon_weight_grad(self._h, ctypes.byref(args), ctypes.c_void_p(_stream(stream, self.device))),
-                    "muon_weight_grad")
+        self._check(lib().muon_weight_grad(self._h, args, _stream(stream, self.device)), "muon_weight_grad")
         return G
 
     def sync(self, stream=None):
