@@ -281,7 +281,7 @@ typedef struct {
  * head_dim: a multiple of 8, at most 128.  scale: finite and > 0.  q, k, v: read; out:
  * written; lse: fp32 [n_heads][total_q], written; max_logits: n_heads floats or NULL,
  * updated in place (start an optimizer step's micro-batches from -inf; a NaN logit is
- * passed over).  out, lse and max_logits may not overlap any buffer of the call
+ * passed over with its row).  out, lse and max_logits may not overlap any buffer of the call
  * (strided views that interleave without sharing an element do not overlap).
  * Non-finite values in a sequence's own rows reach its outputs; the values of one
  * sequence, and of rows in none, never reach another's.

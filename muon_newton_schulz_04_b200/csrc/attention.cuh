@@ -90,6 +90,31 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         : "memory");
 }
 
+// Moves registers between the warpgroups of a block: every warp of a warpgroup takes N from
+// here on.  The sum over the block stays within what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// Barrier `id` of the block for `threads` threads.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+        " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- products of tiles
@@ -107,14 +132,22 @@ __device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b)
     }
 }
 
-// D (+)= A * B: A 128 x 128 bf16 in tensor memory, B a 128-row tile of DP columns.
+// D (+)= A_h * B_h: half h (64 of the 128 rows of B) of the contraction, A_h 128 x 64 bf16 in
+// tensor memory.
 template <int DP>
-__device__ __forceinline__ void mma_tb(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+__device__ __forceinline__ void mma_tb_half(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int h, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
 #pragma unroll
-    for (int kk = 0; kk < AT_ROWS / 16; ++kk)
-        tc_mma_f16_ts(d_tmem, a_tmem + 8 * kk, smem_desc_sw128(b + (uint32_t)kk * 2048u, AT_CHUNK, 1024), idesc,
+    for (int kk = 0; kk < 4; ++kk)
+        tc_mma_f16_ts(d_tmem, a_tmem + 8u * kk, smem_desc_sw128(b + (uint32_t)(4 * h + kk) * 2048u, AT_CHUNK, 1024), idesc,
                       accumulate || kk != 0);
+}
+
+// 64 fp32 columns of this thread's row.
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
+    tmem_ld_32x32b_x32(taddr, v[0]);
+    tmem_ld_32x32b_x32(taddr + 32u, v[1]);
+    tmem_ld_wait();
 }
 
 // Zeroes rows [first, 128) of a tile of DP columns; called by `threads` threads, `t` this one's
@@ -156,6 +189,40 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// Largest of three; NaN when one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// 2^x of two values on the FMA pipe, which has time to spare beside the special function unit:
+// x = n + f with n the nearest integer (Cody-Waite), 2^f by its minimax polynomial of degree 4
+// on [-1/2, 1/2] (Remez exchange; relative error 2.6e-6), n added to the exponent.  Finite x
+// below -126 gives 2^-126, as does -inf; NaN, +inf and x >= 128 give no meaningful value.
+__device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
+    float x, y;
+    unpack2(x2, x, y);
+    x2 = pack2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+    constexpr float MAGIC = 12582912.f;         // 1.5 * 2^23: the sum's low bits are the nearest integer
+    const uint64_t t2 = add2(x2, pack2(MAGIC, MAGIC));
+    const uint64_t f2 = fma2(add2(t2, pack2(-MAGIC, -MAGIC)), pack2(-1.f, -1.f), x2);
+    uint64_t p2 = fma2(f2, pack2(0x1.3997d6p-7f, 0x1.3997d6p-7f), pack2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
+    p2 = fma2(p2, f2, pack2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
+    p2 = fma2(p2, f2, pack2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
+    p2 = fma2(p2, f2, pack2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+    float tx, ty, px, py;
+    unpack2(t2, tx, ty);
+    unpack2(p2, px, py);
+    a = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
+    b = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

@@ -29,22 +29,11 @@ constexpr int ERR_BW_LOAD = 0x211, ERR_BW_MMA = 0x212, ERR_BW_MATH = 0x213;
 
 __device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// D = A B: A 128 x 128 bf16 in tensor memory as two halves of 64 columns of the
-// contraction, 64 tensor memory columns apart.
+// D (+)= A B: A 128 x 128 bf16 in tensor memory, its halves 64 columns apart.
 template <int DP>
 __device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
-#pragma unroll
-    for (int kk = 0; kk < AT_ROWS / 16; ++kk)
-        tc_mma_f16_ts(d_tmem, a_tmem + 64u * (kk / 4) + 8u * (kk % 4),
-                      smem_desc_sw128(b + (uint32_t)kk * 2048u, AT_CHUNK, 1024), idesc, accumulate || kk != 0);
-}
-
-// 64 fp32 columns of this thread's row.
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
-    tmem_ld_32x32b_x32(taddr, v[0]);
-    tmem_ld_32x32b_x32(taddr + 32u, v[1]);
-    tmem_ld_wait();
+    mma_tb_half<DP>(d_tmem, a_tmem, b, 0, accumulate);
+    mma_tb_half<DP>(d_tmem, a_tmem + 64u, b, 1, true);
 }
 
 // Writes `n` accumulator columns from `col` of this thread's row, times f, as bf16.
