@@ -230,4 +230,46 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Writes 32 rows of one half (DP / 2 columns) of an fp32 accumulator as bf16: the warp's
+// lanes hold a row each, `taddr` the half's first column in tensor memory, f the row's factor
+// (`zero`: the row is 0 whatever the accumulator holds).  Rows first .. first + 31 of the tile
+// go through its 128-byte lines at `stage` (a q, k or v tile that no product reads any more;
+// 16-byte unit u of row r at u ^ (r & 7)), so that each store of the warp covers whole rows:
+// storing from a row per lane takes 32 lines a store (for a tile of two 128-wide query tiles,
+// 4500 cycles against 700).  Rows from `live` on and columns from d on are not written.
+template <int DP>
+__device__ __forceinline__ void store_rows(uint32_t taddr, bool any, bool zero, float f, uint32_t stage, int half, int first,
+                                           int live, __nv_bfloat16* g, long long rs, int d) {
+    constexpr int UNITS = DP / 16;                              // 16-byte units of a row's half
+    const int lane = (int)(threadIdx.x & 31u);
+    const uint32_t line = stage + (DP == 128 ? (uint32_t)half * AT_CHUNK : 0u);
+    const int unit0 = DP == 128 ? 0 : 4 * half;
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld_32x32b_x32(taddr + 32u * i, o);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[u] = zero ? 0u : bf16x2(__uint_as_float(o[8 * e + 2 * u]) * f, __uint_as_float(o[8 * e + 2 * u + 1]) * f);
+            sts128(line + (uint32_t)((first + lane) * 128 + ((unit0 + 4 * i + e) ^ (lane & 7)) * 16),
+                   make_uint4(v[0], v[1], v[2], v[3]));
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+        const int r = (32 * k + lane) / UNITS, u = (32 * k + lane) % UNITS, col = half * (DP / 2) + 8 * u;
+        if (first + r < live && col < d)
+            *reinterpret_cast<uint4*>(g + (first + r) * rs + col) =
+                lds128(line + (uint32_t)((first + r) * 128 + ((unit0 + u) ^ (r & 7)) * 16));
+    }
+    __syncwarp();
+}
+
 }  // namespace muon

@@ -36,31 +36,6 @@ __device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uin
     mma_tb_half<DP>(d_tmem, a_tmem + 64u, b, 1, true);
 }
 
-// Writes `n` accumulator columns from `col` of this thread's row, times f, as bf16.
-template <int N>
-__device__ __forceinline__ void store_row(uint32_t taddr, bool any, bool live, float f, int col, int d, __nv_bfloat16* g) {
-#pragma unroll 1
-    for (int i = 0; i < N / 32; ++i) {
-        uint32_t o[32];
-        if (any) {
-            tmem_ld_32x32b_x32(taddr + 32u * i, o);
-            tmem_ld_wait();
-        }
-        if (!live) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = col + 32 * i + 8 * e;
-            if (c < d) {
-                uint32_t v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    v[u] = any ? bf16x2(__uint_as_float(o[8 * e + 2 * u]) * f, __uint_as_float(o[8 * e + 2 * u + 1]) * f) : 0u;
-                *reinterpret_cast<uint4*>(g + c) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        }
-    }
-}
-
 // ============================================================================ dQ
 
 template <int DP>
@@ -299,9 +274,9 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             math_sync();
             if (ok) {
                 if (half == 0 && live) p.delta[stat] = D + exch[t] + exch[128 + t];
-                store_row<DP / 2>(tmem + lane_base + L::DQ_COL + (uint32_t)(half * (DP / 2)), n > 0, live, p.scale,
-                                  half * (DP / 2), p.d,
-                                  p.dq.p + (long long)(q0 + (live ? row : 0)) * p.dq.rs + (long long)head * p.dq.hs);
+                store_rows<DP>(tmem + lane_base + L::DQ_COL + (uint32_t)(half * (DP / 2)), n > 0, n == 0, p.scale,
+                               smem_u32(s_q), half, (int)(warp & 3u) * 32, lq - row0,
+                               p.dq.p + (long long)(q0 + row0) * p.dq.rs + (long long)head * p.dq.hs, p.dq.rs, p.d);
             }
         }
     }
@@ -552,13 +527,13 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tc_fence_after();
             }
             if (ok) {
-                const bool mine = key < lk;
-                const long long r = k0 + (mine ? key : 0);
-                const int col = half * (DP / 2);
-                store_row<DP / 2>(tmem + lane_base + L::DK_COL + (uint32_t)col, n > 0, mine, p.scale, col, p.d,
-                                  p.dk.p + r * p.dk.rs + (long long)kv_head * p.dk.hs);
-                store_row<DP / 2>(tmem + lane_base + L::DV_COL + (uint32_t)col, n > 0, mine, 1.f, col, p.d,
-                                  p.dv.p + r * p.dv.rs + (long long)kv_head * p.dv.hs);
+                const uint32_t col = (uint32_t)(half * (DP / 2));
+                store_rows<DP>(tmem + lane_base + L::DK_COL + col, n > 0, n == 0, p.scale, smem_u32(s_k), half,
+                               (int)(warp & 3u) * 32, lk - key0,
+                               p.dk.p + (long long)(k0 + key0) * p.dk.rs + (long long)kv_head * p.dk.hs, p.dk.rs, p.d);
+                store_rows<DP>(tmem + lane_base + L::DV_COL + col, n > 0, n == 0, 1.f, smem_u32(s_v), half,
+                               (int)(warp & 3u) * 32, lk - key0,
+                               p.dv.p + (long long)(k0 + key0) * p.dv.rs + (long long)kv_head * p.dv.hs, p.dv.rs, p.d);
             }
         }
     }

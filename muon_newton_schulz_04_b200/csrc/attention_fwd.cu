@@ -375,8 +375,9 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             named_sync(1 + w, 256);
             l += *other;
             if (bad || m == INFINITY) l = __uint_as_float(0x7FC00000u);
-            if (ok && nw > 0) {
-                ok = mbar_wait(&o_full[w], 0, abort_flag, p.err, ERR_FW_SOFTMAX);
+            if (ok && nmax > 0) {
+                // q's tile is written over: its products, or without any its load, are done
+                ok = mbar_wait(nw > 0 ? &o_full[w] : q_full, 0, abort_flag, p.err, ERR_FW_SOFTMAX);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             }
@@ -385,29 +386,10 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 // no key seen: the sum is 0, or some 2^-126 from exp2_pair
                 const bool none = m == -INFINITY && l == l;
                 const float inv = none ? 0.f : 1.f / l;
-                __nv_bfloat16* o_g = p.out.p + (long long)(q0 + row) * p.out.rs + (long long)head * p.out.hs;
-#pragma unroll 1
-                for (int i = 0; i < DP / 64; ++i) {
-                    uint32_t o[32];
-                    if (nw > 0) {
-                        tmem_ld_32x32b_x32(o_t + 32u * i, o);
-                        tmem_ld_wait();
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int col = DP / 2 * h + 32 * i + 8 * e;
-                            if (col < p.d) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    v[u] = none ? 0u : bf16x2(__uint_as_float(o[8 * e + 2 * u]) * inv,
-                                                              __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
-                                *reinterpret_cast<uint4*>(o_g + col) = make_uint4(v[0], v[1], v[2], v[3]);
-                            }
-                        }
-                    }
-                }
+                store_rows<DP>(o_t, nw > 0, none, inv, smem_u32(sq) + w * L::TILE, h, (int)(warp & 3u) * 32,
+                               lq - row0 - w * AT_ROWS,
+                               p.out.p + (long long)(q0 + row0 + w * AT_ROWS) * p.out.rs + (long long)head * p.out.hs,
+                               p.out.rs, p.d);
                 if (h == 0) {
                     if (live)
                         p.lse[(size_t)head * p.total_q + q0 + row] =
