@@ -143,6 +143,18 @@ __device__ __forceinline__ void mma_tb_half(uint32_t d_tmem, uint32_t a_tmem, ui
                       accumulate || kk != 0);
 }
 
+// D = A * B_h^T: A a 128-row tile, B_h rows 64 h .. 64 h + 63 of one, contraction along the rows.
+template <int DP>
+__device__ __forceinline__ void mma_abt_half(uint32_t d_tmem, uint32_t a, uint32_t b, int h) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS / 2, 0);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t off = (uint32_t)(kk / 4) * AT_CHUNK + (uint32_t)(kk % 4) * 32u;
+        tc_mma_f16(d_tmem, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off + 8192u * (uint32_t)h, 16, 1024), idesc,
+                   kk != 0);
+    }
+}
+
 // 64 fp32 columns of this thread's row.
 __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
     tmem_ld_32x32b_x32(taddr, v[0]);

@@ -1,23 +1,22 @@
 // attention_fwd.cu -- packed causal attention with grouped heads: O = softmax(S) V, the
 // log-sums of the rows and each head's largest logit.
 //
-// One CTA computes 256 query rows of one head of one sequence, as two tiles of 128 rows with
-// an MMA warp and two softmax warpgroups each, so that one tile's products run beside the
-// other's softmax.  K and V tiles of 128 rows stream through a ring in shared memory.
+// A query tile has 128 rows, an MMA warp and a softmax warpgroup; K and V tiles of 128 rows
+// stream through a ring in shared memory.  For each key tile
 //
 //   S = Q K^T      both operands from shared memory, 128 x 128 fp32 in tensor memory
-//   P = exp(S - m) a thread owns 64 keys of a row: sixteen warps, as eight leave the pipes
-//                  idle between dependent instructions
-//   O += P V       P is written back to tensor memory as bf16 and is the A operand there
+//   P = exp(S - m) a thread owns a row, so its maximum and sum need no exchange
+//   O += P V       P is written back to tensor memory as bf16 and is the A operand there; it
+//                  starts when the first 64 keys of P are there
 //
 // m is the maximum that P and O are scaled by; it follows the true maximum only when that has
 // grown by 2^8, so that O is rescaled rarely (P stays below 2^8; sums and O are fp32, and P's
-// rounding to bf16 is relative).  The two threads of a row tell each other their halves'
-// maxima for every key tile, their sums once at the end.
+// rounding to bf16 is relative).
 //
-// The special function unit forms 16 exponentials a cycle, 128 x 128 in 1024 cycles: as long
-// as the two products of a 128-wide head take, twice as long as those of a 64-wide one.  So
-// some are computed on the FMA pipe instead (exp2_pair).
+// The special function unit takes 8 cycles for a warp's exponentials, 1024 for 128 x 128: as
+// long as the two products of a 128-wide head take, twice as long as those of a 64-wide one.
+// So a quarter of them is computed on the FMA pipe (exp2_pair), at 12 cycles a warp; the best
+// mix of the two gets to 7.5 where the unit alone gets to 8.6.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -26,32 +25,31 @@
 namespace muon {
 namespace {
 
-// 128-wide heads: two query tiles a CTA, one CTA an SM.  64-wide heads: one tile, two CTAs an
-// SM, which also hide each other's start and end (eight sequences of 1024, 25 heads: XX us
-// against XX us with two tiles a CTA).
+// 128-wide heads: two query tiles a CTA, one CTA an SM, and P in the place of S.  64-wide
+// heads: one tile, two CTAs an SM, which also hide each other's start and end, and P apart
+// from S, so that the next S need not wait for P V.
 template <int DP>
 struct FwLayout {
     static constexpr int TILES = DP == 64 ? 1 : 2;
-    static constexpr int SOFTMAX = TILES * 256;                     // softmax threads
+    static constexpr int SOFTMAX = TILES * 128;                     // softmax threads
     static constexpr int THREADS = SOFTMAX + 128;                   // + a warpgroup: TMA, an MMA warp per tile, tensor memory
     static constexpr int CTAS = 2 / TILES;                          // of an SM
     static constexpr int W_TMA = SOFTMAX / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 3;
     // registers a thread: at launch, then of the softmax warpgroups and the other one
-    static constexpr int REGS = TILES == 1 ? 80 : 96;
-    static constexpr int REGS_SOFTMAX = TILES == 1 ? 96 : 104, REGS_OTHER = TILES == 1 ? 48 : 56;
+    static constexpr int REGS = TILES == 1 ? 128 : 168;
+    static constexpr int REGS_SOFTMAX = TILES == 1 ? 216 : 232, REGS_OTHER = 40;
     static_assert(SOFTMAX * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS, "more registers than launched with");
     static constexpr int TILE = DP / 64 * AT_CHUNK;                 // bytes of a q, k or v tile
     static constexpr int SLOTS = 5;                                 // ring of k and v tiles
     static constexpr int BARRIERS = 1 + 2 * SLOTS + 6 * TILES;
-    static constexpr int SMEM = (TILES + SLOTS) * TILE + 8 * BARRIERS + TILES * 256 * 4 + 64;
-    // 64-wide heads leave room for P beside S, so the next S need not wait for P V
+    static constexpr int SMEM = (TILES + SLOTS) * TILE + 8 * BARRIERS + 64;
     static constexpr bool P_APART = DP == 64;
     static constexpr uint32_t TMEM_COLS = 512 / CTAS;
     static constexpr uint32_t S_COL = 0;                            // + 128 per tile
-    static constexpr uint32_t P_COL = P_APART ? 128 : 0;            // + P_STEP per tile, P_HALF per 64 keys
-    static constexpr uint32_t P_STEP = 128, P_HALF = P_APART ? 32 : 64;
+    static constexpr uint32_t P_COL = P_APART ? 128 : 0;            // + 128 per tile, P_HALF per 64 keys
+    static constexpr uint32_t P_HALF = P_APART ? 32 : 64;
     static constexpr uint32_t O_COL = P_APART ? 192 : 256;          // + DP per tile
-    static constexpr int ON_FMA = DP == 64 ? 3 : 2;                 // of 8 pairs of exponentials
+    static constexpr int ON_FMA = DP == 64 ? 2 : 1;                 // of 8 pairs of exponentials
     static_assert(SMEM <= 232448 / CTAS - (CTAS - 1) * 1024, "shared memory above the SM's 228 KiB");
 };
 
@@ -85,12 +83,11 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     uint64_t* full = q_full + 1;
     uint64_t* empty = full + L::SLOTS;
     uint64_t* s_full = empty + L::SLOTS;        // per tile, as the following ones
-    uint64_t* s_read = s_full + TILES;       // the softmax has S in registers (P_APART)
-    uint64_t* p_ready = s_read + TILES;      // per tile and half
-    uint64_t* pv_done = p_ready + 2 * TILES; // P has been read, O holds it
+    uint64_t* s_read = s_full + TILES;          // the softmax has S in registers (P_APART)
+    uint64_t* p_ready = s_read + TILES;         // two: for each half of the keys
+    uint64_t* pv_done = p_ready + 2 * TILES;    // P has been read, O holds it
     uint64_t* o_full = pv_done + TILES;
-    float* exch = reinterpret_cast<float*>(o_full + TILES);      // per tile: a float of each softmax thread
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(exch + TILES * 256);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + TILES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
     int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
@@ -120,11 +117,11 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         }
         for (int i = 0; i < TILES; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_read[i], 256);
-            mbar_init(&o_full[i], 1);
+            mbar_init(&s_read[i], 128);
             mbar_init(&p_ready[2 * i], 128);
             mbar_init(&p_ready[2 * i + 1], 128);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&o_full[i], 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -184,7 +181,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 const int w = (int)warp - L::W_MMA, nw = n[w], kw = keys[w];
                 bool ok = mbar_wait(q_full, 0, abort_flag, p.err, ERR_FW_MMA);
                 const uint32_t q_s = smem_u32(sq) + w * L::TILE, ring_s = smem_u32(ring);
-                const uint32_t s_t = tmem + L::S_COL + 128u * w, p_t = tmem + L::P_COL + L::P_STEP * w,
+                const uint32_t s_t = tmem + L::S_COL + 128u * w, p_t = tmem + L::P_COL + 128u * w,
                                o_t = tmem + L::O_COL + (uint32_t)(DP * w);
                 // ring position of K_j and V_j
                 auto k_at = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
@@ -194,48 +191,38 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 };
                 auto tile_s = [&](int at) { return ring_s + (uint32_t)(at % L::SLOTS) * L::TILE; };
                 auto do_s = [&](int j) {
+                    if (!wait_full(k_at(j))) return false;
                     tc_fence_after();
                     mma_abt<DP>(s_t, q_s, tile_s(k_at(j)));
                     tc_commit(&s_full[w]);
-                };
-                // a tile that is done still passes the other one's K and V on, once they have arrived
-                auto release = [&](int at, bool used) {
-                    if (used) tc_commit(&empty[at % L::SLOTS]);
-                    else if (wait_full(at)) mbar_arrive(&empty[at % L::SLOTS]);
-                    else return false;
+                    tc_commit(&empty[k_at(j) % L::SLOTS]);
                     return true;
                 };
-                if (nw > 0) {
-                    ok = ok && wait_full(0);
-                    if (ok) do_s(0);
+                if (nw > 0) ok = ok && do_s(0);
+                for (int j = 0; j < nw && ok; ++j) {
+                    if (L::P_APART && j + 1 < nw)
+                        ok = mbar_wait(&s_read[w], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA) && do_s(j + 1);
+                    ok = ok && wait_full(v_at(j));
+                    // a last tile of 64 keys at most leaves its upper half out
+                    const int halves = kw - j * AT_ROWS > 64 ? 2 : 1;
+                    for (int h = 0; h < halves && ok; ++h) {
+                        if (!(ok = mbar_wait(&p_ready[2 * w + h], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA))) break;
+                        tc_fence_after();
+                        mma_tb_half<DP>(o_t, p_t + L::P_HALF * h, tile_s(v_at(j)), h, j > 0 || h > 0);
+                    }
+                    if (!ok) break;
+                    tc_commit(&pv_done[w]);
+                    tc_commit(&empty[v_at(j) % L::SLOTS]);
+                    if (j + 1 == nw) tc_commit(&o_full[w]);
+                    // S takes P's place: products run in order, so P V has read it
+                    if (!L::P_APART && j + 1 < nw) ok = do_s(j + 1);
                 }
-                ok = ok && release(0, nw > 0);
-                for (int j = 0; j < nmax && ok; ++j) {
-                    const bool next = j + 1 < nw;
-                    if (L::P_APART && next) {
-                        ok = wait_full(k_at(j + 1)) && mbar_wait(&s_read[w], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA);
-                        if (!ok) break;
-                        do_s(j + 1);
-                    }
-                    if (j < nw) {
-                        if (!(ok = wait_full(v_at(j)))) break;
-                        const int halves = kw - j * AT_ROWS > 64 ? 2 : 1;
-                        for (int h = 0; h < halves; ++h) {
-                            // (the half without keys, of a last tile with 64 at most, takes no part)
-                            if (!(ok = mbar_wait(&p_ready[2 * w + h], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA))) break;
-                            tc_fence_after();
-                            mma_tb_half<DP>(o_t, p_t + L::P_HALF * h, tile_s(v_at(j)), h, j > 0 || h > 0);
-                        }
-                        if (!ok) break;
-                        tc_commit(&pv_done[w]);
-                        if (!next) tc_commit(&o_full[w]);
-                    }
-                    if (!L::P_APART && next) {
-                        // S takes P's place: products run in order, so P V has read it
-                        if (!(ok = wait_full(k_at(j + 1)))) break;
-                        do_s(j + 1);
-                    }
-                    ok = release(v_at(j), j < nw) && (j + 1 == nmax || release(k_at(j + 1), next));
+                // a tile that is done still passes the other one's K and V on, once they have arrived
+                for (int at = nw == 0 ? 0 : 2 * nw - 1; at < 2 * nmax && ok; ++at) {
+                    if (nw > 0 && nw < nmax && at == 2 * nw) continue;      // V of its last tile
+                    if (nw > 0 && nw == nmax) break;
+                    ok = wait_full(at);
+                    if (ok) mbar_arrive(&empty[at % L::SLOTS]);
                 }
                 if (!ok || *abort_flag) spin_ns_at_most(2000000ull);    // products in flight end
             }
@@ -243,69 +230,67 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             regs_less<L::REGS_OTHER>();
         } else {
             regs_more<L::REGS_SOFTMAX>();
-            const int w = (int)(warp >> 3), h = (int)(warp >> 2) & 1, t = (int)(threadIdx.x & 127u);
+            const int w = (int)(warp >> 2), t = (int)(threadIdx.x & 127u);
             const uint32_t lane_base = (warp & 3u) * 32u << 16;
             const int row = row0 + w * AT_ROWS + t;                 // in the sequence
-            const uint32_t s_t = tmem + lane_base + L::S_COL + 128u * w + 64u * h,
-                           p_t = tmem + lane_base + L::P_COL + L::P_STEP * w + L::P_HALF * h,
-                           o_t = tmem + lane_base + L::O_COL + (uint32_t)(DP * w + DP / 2 * h);
-            float* mine = exch + 256 * w + 128 * h + t;             // and the row's other thread's
-            const float* other = exch + 256 * w + 128 * (h ^ 1) + t;
+            const uint32_t s_t = tmem + lane_base + L::S_COL + 128u * w, p_t = tmem + lane_base + L::P_COL + 128u * w,
+                           o_t = tmem + lane_base + L::O_COL + (uint32_t)(DP * w);
             const float c = p.scale * AT_LOG2E;
-            const int see = row + shift - 64 * h;                   // last key that this row sees, from this half on
-            const int all_see = row0 + w * AT_ROWS + shift + 1 - 64 * h;
+            const int see = row + shift;                            // last key that this row sees
+            const int all_see = row0 + w * AT_ROWS + shift + 1;     // keys that all rows see
             float m = -INFINITY, top = -INFINITY;                   // scaled by; true maximum
             float l = 0.f;
             bool ok = true, bad = false;                            // bad: a NaN among the logits
             const int nw = n[w];
-            // The tiles' exponentials take turns (barriers 11 and 12): left alone, both would form them
-            // at the same time and then wait for the products at the same time.
-            if (TILES == 2 && w == 1 && nmin > 0) named_arrive(11, 512);
+            auto wait = [&](uint64_t* bar, int use) {
+                ok = ok && mbar_wait(bar, (uint32_t)use & 1u, abort_flag, p.err, ERR_FW_SOFTMAX);
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            // The tiles' exponentials take turns (barriers 1 and 2): left alone, both would form them at
+            // the same time and then wait for their products at the same time.
+            if (TILES == 2 && w == 1 && nmin > 0) named_arrive(1, 256);
             // A warp whose wait gave up goes on without waiting: the others meet it in the barriers.
             for (int j = 0; j < nw; ++j) {
-                ok = ok && mbar_wait(&s_full[w], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_SOFTMAX);
-                ok = __all_sync(0xffffffffu, ok);
+                wait(&s_full[w], j);
                 tc_fence_after();
                 const int key0 = j * AT_ROWS;
-                const bool edge = key0 + 64 > all_see;
-                float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t s[4][32];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t s[32];
-                    tmem_ld_32x32b_x32(s_t + 32u * q, s);
-                    tmem_ld_wait();
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + 32 * q + i > see) s[i] = 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x4[e] = max3_nan(x4[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_t + 32u * i, s[i]);
+                tmem_ld_wait();
+                if (L::P_APART) {
+                    tc_fence_before();
+                    mbar_arrive(&s_read[w]);
                 }
-                float mx = max_nan(max_nan(x4[0], x4[1]), max_nan(x4[2], x4[3]));
-                *mine = mx;
-                named_sync(1 + w, 256);
-                // (the next tile's S comes after every thread's P or s_read of this one: nobody
-                // overwrites this before it is read)
-                mx = max_nan(mx, *other);
+                if (key0 + AT_ROWS > all_see) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (key0 + i > see) s[i / 32][i % 32] = 0xFF800000u;
+                }
+                float x8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x8[e] = max_nan(__uint_as_float(s[0][2 * e]), __uint_as_float(s[0][2 * e + 1]));
+#pragma unroll
+                for (int i = 16; i < 128; i += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x8[e] = max3_nan(x8[e], __uint_as_float(s[i / 32][i % 32 + 2 * e]),
+                                         __uint_as_float(s[i / 32][i % 32 + 2 * e + 1]));
+                const float mx = max3_nan(max3_nan(x8[0], x8[1], x8[2]), max3_nan(x8[3], x8[4], x8[5]), max_nan(x8[6], x8[7]));
                 bad = bad || mx != mx;
                 top = fmaxf(top, mx);
+                const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * c > 8.f;
                 if (L::P_APART && j > 0) {                          // the P before has been read
-                    ok = ok && mbar_wait(&pv_done[w], (uint32_t)(j - 1) & 1u, abort_flag, p.err, ERR_FW_SOFTMAX);
-                    ok = __all_sync(0xffffffffu, ok);
+                    wait(&pv_done[w], j - 1);
                     tc_fence_after();
                 }
-                const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * c > 8.f;
-                if (__any_sync(0xffffffffu, grow)) {                // the same warp of the other half does the same
+                if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? (m == -INFINITY ? 0.f : ex2((m - top) * c)) : 1.f;
                     if (grow) m = top;
                     l *= f;
-                    if (j > 0) {
+                    if (j > 0) {                                    // (S of this tile came after P V of the last one)
 #pragma unroll 1
-                        for (int i = 0; i < DP / 64; ++i) {
+                        for (int i = 0; i < DP / 32; ++i) {
                             uint32_t o[32];
                             tmem_ld_32x32b_x32(o_t + 32u * i, o);
                             tmem_ld_wait();
@@ -313,33 +298,25 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                             tmem_st_32x32b_x32(o_t + 32u * i, o);
                         }
-                        // neither half's P is given out before both halves of O's columns are scaled
-                        tmem_st_wait();
-                        tc_fence_before();
-                        named_sync(3 + 4 * w + (int)(warp & 3u), 64);
                     }
                 }
-                if (TILES == 2 && j < nmin) named_sync(11 + w, 512);
+                if (lk - key0 < AT_ROWS) {
+                    // rows behind the sequence's keys: P is 0 there, but 0 times what lies behind need not be
+                    const int at = j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2;
+                    wait(&full[at % L::SLOTS], at / L::SLOTS);
+                    zero_rows<DP>(smem_u32(ring + (at % L::SLOTS) * L::TILE), lk - key0, t, 128);
+                    fence_proxy_async_smem();
+                }
                 const float base = m == -INFINITY ? 0.f : m * c;
                 const uint64_t c2 = pack2(c, c), b2 = pack2(-base, -base);
                 uint64_t sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+                if (TILES == 2 && j < nmin) named_sync(1 + w, 256);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t s[32], pr[16];
-                    tmem_ld_32x32b_x32(s_t + 32u * q, s);
-                    tmem_ld_wait();
-                    if (L::P_APART && q == 1) {
-                        tc_fence_before();
-                        mbar_arrive(&s_read[w]);
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + 32 * q + i > see) s[i] = 0xFF800000u;
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pr[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint64_t x2 = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, b2);
+                        const uint64_t x2 = fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, b2);
                         float x, y;
                         if (i % 8 < L::ON_FMA) {
                             exp2_pair(x2, x, y);
@@ -351,29 +328,18 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                         sum2[i & 1] = add2(sum2[i & 1], pack2(x, y));
                         pr[i] = bf16x2(x, y);
                     }
-                    tmem_st_32x32b_x16(p_t + 16u * q, pr);
+                    tmem_st_32x32b_x16(p_t + L::P_HALF * (q / 2) + 16u * (q % 2), pr);
+                    if (q == 3 && TILES == 2 && j + w < nmin) named_arrive(2 - w, 256);
+                    if (q % 2 == 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&p_ready[2 * w + q / 2]);
+                    }
                 }
-                if (TILES == 2 && j + w < nmin) named_arrive(12 - w, 512);
                 float a, b;
                 unpack2(add2(sum2[0], sum2[1]), a, b);
                 l += a + b;
-                if (lk - key0 < AT_ROWS) {
-                    // rows behind the sequence's keys: P is 0 there, but 0 times what lies behind need not be
-                    const int at = j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2;
-                    ok = ok && mbar_wait(&full[at % L::SLOTS], (uint32_t)(at / L::SLOTS) & 1u, abort_flag, p.err, ERR_FW_SOFTMAX);
-                    ok = __all_sync(0xffffffffu, ok);
-                    zero_rows<DP>(smem_u32(ring + (at % L::SLOTS) * L::TILE), lk - key0, t, 128);
-                    fence_proxy_async_smem();
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&p_ready[2 * w + h]);
             }
-            // the row's sum over both halves
-            named_sync(1 + w, 256);
-            *mine = bad || m == INFINITY ? __uint_as_float(0x7FC00000u) : l;
-            named_sync(1 + w, 256);
-            l += *other;
             if (bad || m == INFINITY) l = __uint_as_float(0x7FC00000u);
             if (ok && nmax > 0) {
                 // q's tile is written over: its products, or without any its load, are done
@@ -386,20 +352,19 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 // no key seen: the sum is 0, or some 2^-126 from exp2_pair
                 const bool none = m == -INFINITY && l == l;
                 const float inv = none ? 0.f : 1.f / l;
-                store_rows<DP>(o_t, nw > 0, none, inv, smem_u32(sq) + w * L::TILE, h, (int)(warp & 3u) * 32,
-                               lq - row0 - w * AT_ROWS,
-                               p.out.p + (long long)(q0 + row0 + w * AT_ROWS) * p.out.rs + (long long)head * p.out.hs,
-                               p.out.rs, p.d);
-                if (h == 0) {
-                    if (live)
-                        p.lse[(size_t)head * p.total_q + q0 + row] =
-                            none ? -INFINITY : (m == -INFINITY ? 0.f : m * p.scale) + logf(l);
-                    if (p.max_logits != nullptr) {
-                        float best = live && l == l ? top : -INFINITY;      // a row with a NaN is passed over
+                for (int h = 0; h < 2; ++h)
+                    store_rows<DP>(o_t + (uint32_t)(DP / 2 * h), nw > 0, none, inv, smem_u32(sq) + w * L::TILE, h,
+                                   (int)(warp & 3u) * 32, lq - row0 - w * AT_ROWS,
+                                   p.out.p + (long long)(q0 + row0 + w * AT_ROWS) * p.out.rs + (long long)head * p.out.hs,
+                                   p.out.rs, p.d);
+                if (live)
+                    p.lse[(size_t)head * p.total_q + q0 + row] =
+                        none ? -INFINITY : (m == -INFINITY ? 0.f : m * p.scale) + logf(l);
+                if (p.max_logits != nullptr) {
+                    float best = live && l == l ? top : -INFINITY;          // a row with a NaN is passed over
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-                        if ((t & 31) == 0 && best > -INFINITY) atomic_max_float(p.max_logits + head, best * p.scale);
-                    }
+                    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+                    if ((t & 31) == 0 && best > -INFINITY) atomic_max_float(p.max_logits + head, best * p.scale);
                 }
             }
         }
