@@ -183,29 +183,37 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             const bool live = row < lq;
             const size_t stat = (size_t)head * p.total_q + q0 + (live ? row : 0);
             const float c = p.scale * AT_LOG2E;
-            // D of the row: each of its two threads sums one half
-            float dsum = 0.f;
-            if (live) {
-                const long long at_g = (long long)(q0 + row) * p.go.rs + (long long)head * p.go.hs;
-                const long long at_o = (long long)(q0 + row) * p.out.rs + (long long)head * p.out.hs;
+            // D of the rows: a warp takes 16 of them, 16 bytes a lane, all loads in flight at once (a row per
+            // thread reads 32 lines a load: 12000 cycles)
+            {
+                constexpr int LANES = DP / 8, ROWS = 32 / LANES, TURNS = 16 / ROWS;
+                const int lane = t & 31, r0 = (int)warp * 16 + lane / LANES, col = lane % LANES * 8;
+                uint4 x[TURNS], y[TURNS];
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const int col = half * (DP / 2) + 8 * i;
-                    if (col < p.d) {
-                        const uint4 a = *reinterpret_cast<const uint4*>(p.go.p + at_g + col);
-                        const uint4 b = *reinterpret_cast<const uint4*>(p.out.p + at_o + col);
-                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            dsum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), dsum);
-                            dsum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), dsum);
-                        }
+                for (int i = 0; i < TURNS; ++i) {
+                    const long long r = row0 + r0 + i * ROWS;
+                    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+                    if (r < lq && col < p.d) {
+                        x[i] = *reinterpret_cast<const uint4*>(p.go.p + (q0 + r) * p.go.rs + (long long)head * p.go.hs + col);
+                        y[i] = *reinterpret_cast<const uint4*>(p.out.p + (q0 + r) * p.out.rs + (long long)head * p.out.hs + col);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < TURNS; ++i) {
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, v[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), sum);
+                        sum = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), sum);
+                    }
+#pragma unroll
+                    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane % LANES == 0) exch[r0 + i * ROWS] = sum;
+                }
             }
-            exch[half * 128 + t] = dsum;
             math_sync();
-            const float D = exch[t] + exch[128 + t];
+            const float D = exch[t];
             const float lse2 = live ? p.lse[stat] * AT_LOG2E : 0.f;
             const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-D, -D);
             float rest = 0.f;                   // sum of dS: 0 but for the rounding of O in D
@@ -440,13 +448,12 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             auto fetch = [&](int tl, int hd) {
                 const int row = tl * AT_ROWS + t;
                 if (row >= lq) return 0.f;
-                const size_t at = (size_t)hd * p.total_q + q0 + row;
-                return half == 0 ? -p.lse[at] * AT_LOG2E : -p.delta[at];
+                return (half == 0 ? p.lse : p.delta)[(size_t)hd * p.total_q + q0 + row];
             };
-            float next = n > 0 ? fetch(tile, head) : 0.f;
+            float next = n > 0 ? fetch(tile, head) : 0.f;           // (used an item later: nothing waits for it)
             for (int it = 0; it < n; ++it) {
                 float* st = stats + (it & 1) * 256;
-                st[half * 128 + t] = next;
+                st[half * 128 + t] = half == 0 ? -AT_LOG2E * next : -next;
                 math_sync();
                 const int row0 = tile * AT_ROWS;
                 if (++tile == tiles) { tile = first; ++head; }
@@ -454,7 +461,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 // query i of the tile sees this thread's key when i >= unseen; rows from lq on are none
                 const int unseen = key - shift - row0 - 64 * half, live = lq - row0 - 64 * half;
                 const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + AT_ROWS > lq;
-                const uint32_t lse_s = smem_u32(st + 64 * half), d_s = smem_u32(st + 128 + 64 * half);
+                const float4* lse4 = reinterpret_cast<const float4*>(st + 64 * half);
+                const float4* d4 = reinterpret_cast<const float4*>(st + 128 + 64 * half);
 
                 // a warp whose wait gave up goes on without waiting: the others meet it in math_sync
                 ok = ok && mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
@@ -465,21 +473,24 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 uint32_t pr[32];
 #pragma unroll
                 for (int i = 0; i < 64; i += 4) {
-                    const uint4 l4 = lds128(lse_s + 4u * i);
-                    float x[4];
-                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2,
-                                 pack2(__uint_as_float(l4.x), __uint_as_float(l4.y))), x[0], x[1]);
-                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32 + 2]), __uint_as_float(s[i / 32][i % 32 + 3])), c2,
-                                 pack2(__uint_as_float(l4.z), __uint_as_float(l4.w))), x[2], x[3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = ex2(x[e]);
-                        if (edge && (i + e < unseen || i + e >= live)) x[e] = 0.f;
-                        s[i / 32][i % 32 + e] = __float_as_uint(x[e]);
-                    }
-                    pr[i / 2] = bf16x2(x[0], x[1]);
-                    pr[i / 2 + 1] = bf16x2(x[2], x[3]);
+                    uint32_t* x = &s[i / 32][i % 32];
+                    const float4 l4 = lse4[i / 4];
+                    float a, b;
+                    unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, pack2(l4.x, l4.y)), a, b);
+                    x[0] = __float_as_uint(ex2(a));
+                    x[1] = __float_as_uint(ex2(b));
+                    unpack2(fma2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, pack2(l4.z, l4.w)), a, b);
+                    x[2] = __float_as_uint(ex2(a));
+                    x[3] = __float_as_uint(ex2(b));
                 }
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i < unseen || i >= live) s[i / 32][i % 32] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    pr[i] = bf16x2(__uint_as_float(s[i / 16][2 * i % 32]), __uint_as_float(s[i / 16][2 * i % 32 + 1]));
                 tmem_st_32x32b_x32(s_t, pr);
                 if (row0 + AT_ROWS > lq) {
                     // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
@@ -498,23 +509,22 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tc_fence_after();
                 uint32_t dp[2][32];
                 load64(dp_t, dp);
+                if (edge) {         // P is 0 there, but dP - D of a row of no sequence need not be finite
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i < unseen || i >= live) dp[i / 32][i % 32] = 0u;
+                }
 #pragma unroll
                 for (int i = 0; i < 64; i += 4) {
-                    const uint4 d4 = lds128(d_s + 4u * i);
-                    float x[4];
-                    unpack2(mul2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])),
-                                 add2(pack2(__uint_as_float(dp[i / 32][i % 32]), __uint_as_float(dp[i / 32][i % 32 + 1])),
-                                      pack2(__uint_as_float(d4.x), __uint_as_float(d4.y)))), x[0], x[1]);
-                    unpack2(mul2(pack2(__uint_as_float(s[i / 32][i % 32 + 2]), __uint_as_float(s[i / 32][i % 32 + 3])),
-                                 add2(pack2(__uint_as_float(dp[i / 32][i % 32 + 2]), __uint_as_float(dp[i / 32][i % 32 + 3])),
-                                      pack2(__uint_as_float(d4.z), __uint_as_float(d4.w)))), x[2], x[3]);
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i + e < unseen || i + e >= live) x[e] = 0.f;
-                    }
-                    pr[i / 2] = bf16x2(x[0], x[1]);
-                    pr[i / 2 + 1] = bf16x2(x[2], x[3]);
+                    const uint32_t *x = &s[i / 32][i % 32], *y = &dp[i / 32][i % 32];
+                    const float4 e4 = d4[i / 4];
+                    float a, b;
+                    unpack2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                 add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(e4.x, e4.y))), a, b);
+                    pr[i / 2] = bf16x2(a, b);
+                    unpack2(mul2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                 add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(e4.z, e4.w))), a, b);
+                    pr[i / 2 + 1] = bf16x2(a, b);
                 }
                 tmem_st_32x32b_x32(dp_t, pr);
                 tmem_st_wait();
