@@ -121,6 +121,11 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // Tiles lie in shared memory as 64-column chunks of AT_CHUNK bytes, 128-byte swizzled, one
 // 128-byte line per row.
 
+// Shared-memory descriptor of a tile without swizzle (see smem_desc_sw128).
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return smem_desc_sw128(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61);
+}
+
 // D = A * B^T over `dp` columns: A and B 128-row tiles with the contraction along their rows.
 template <int DP>
 __device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b) {

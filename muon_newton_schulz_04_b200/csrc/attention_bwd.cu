@@ -10,6 +10,12 @@
 // dV, dK: four).  Forming S and dP twice costs seven products instead of five; in exchange
 // there is no fp32 dQ in memory to add to (for 128-wide heads 64 KiB a tile pair).
 //
+// In the second kernel a row of the accumulators is a key, and lse and D belong to its columns.
+// They enter through the products themselves: Q gets three more columns with -lse / scale
+// split into three bf16 (24 bits), dO three with -D, K and V three of ones, one more MMA step
+// each.  Read from shared memory instead, beside the tiles that the products read there, they
+// took as long as the exponentials (3720 cycles a tile pair of 128-wide heads against XX).
+//
 // In both, P and dS go back to tensor memory as bf16 in the place of the fp32 tile that they
 // were formed from, and are the A operand there: only Q, K, V and dO tiles lie in shared
 // memory.  Eight warps form P and dS: warp w owns rows 32 (w % 4) .., warps 0-3 the first 64
@@ -34,6 +40,18 @@ template <int DP>
 __device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
     mma_tb_half<DP>(d_tmem, a_tmem, b, 0, accumulate);
     mma_tb_half<DP>(d_tmem, a_tmem + 64u, b, 1, true);
+}
+
+// One more K step of 16: D += A B^T of two 128 x 16 tiles without swizzle (core matrices of 8
+// rows x 16 bytes, the two of a row 2048 bytes apart, groups of 8 rows 128 bytes apart).
+__device__ __forceinline__ void mma_extra(uint32_t d_tmem, uint32_t a, uint32_t b) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS, 0);
+    tc_mma_f16(d_tmem, smem_desc_plain(a, 2048, 128), smem_desc_plain(b, 2048, 128), idesc, 1u);
+}
+
+// Byte of column c of row r of such a tile.
+__device__ __forceinline__ uint32_t extra_at(int r, int c) {
+    return (uint32_t)((c >> 3) * 2048 + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2);
 }
 
 // ============================================================================ dQ
@@ -302,8 +320,9 @@ template <int DP>
 struct DkvLayout {
     static constexpr int TILE = DP / 64 * AT_CHUNK;
     static constexpr int SLOTS = DP == 64 ? 3 : 2;              // of q and of dO
-    static constexpr int BARRIERS = 1 + 4 * SLOTS + 5;
-    static constexpr int SMEM = 1024 + (2 + 2 * SLOTS) * TILE + 8 * BARRIERS + 4 * 128 * 4 + 64;
+    static constexpr int BARRIERS = 2 + 4 * SLOTS + 5;
+    static constexpr int EXTRA = 128 * 16 * 2;                  // 16 more columns of a tile
+    static constexpr int SMEM = 1024 + 5 * EXTRA + (2 + 2 * SLOTS) * TILE + 8 * BARRIERS + 64;
     static constexpr uint32_t S_COL = 0, DP_COL = 128, DK_COL = 256, DV_COL = 384;
     static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
 };
@@ -314,10 +333,12 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     using L = DkvLayout<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *s_k = smem, *s_v = s_k + L::TILE, *s_q = s_v + L::TILE, *s_do = s_q + L::SLOTS * L::TILE;
-    float* stats = reinterpret_cast<float*>(s_do + L::SLOTS * L::TILE);     // two buffers of [lse * log2(e) | D]
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * 128);
-    uint64_t *q_full = kv_full + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
+    // the extra columns: ones beside K and V, two turns of those beside Q and beside dO
+    uint8_t *s_ones = smem, *s_lse = s_ones + L::EXTRA, *s_d = s_lse + 2 * L::EXTRA;
+    uint8_t *s_k = smem + 5 * L::EXTRA, *s_v = s_k + L::TILE, *s_q = s_v + L::TILE, *s_do = s_q + L::SLOTS * L::TILE;
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(s_do + L::SLOTS * L::TILE);
+    uint64_t* extra_ready = kv_full + 1;        // the ones, and the first item's columns
+    uint64_t *q_full = extra_ready + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
     uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 1,
              *dkv_full = ds_ready + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkv_full + 1);
@@ -344,6 +365,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     }
     if (threadIdx.x == 32) {
         mbar_init(kv_full, 1);
+        mbar_init(extra_ready, BW_MATH);
         for (int i = 0; i < L::SLOTS; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -406,12 +428,24 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     tc_fence_after();
                     return ok;
                 };
+                // S^T - lse / scale and dP^T - D
+                const uint32_t ones_s = smem_u32(s_ones), lse_s = smem_u32(s_lse), d_s = smem_u32(s_d);
+                auto do_s_product = [&](int it, uint32_t q) {
+                    mma_abt<DP>(tmem + L::S_COL, k_s, q);
+                    mma_extra(tmem + L::S_COL, ones_s, lse_s + (uint32_t)(it & 1) * L::EXTRA);
+                    tc_commit(s_full);
+                };
+                auto do_dp_product = [&](int it, uint32_t dout) {
+                    mma_abt<DP>(tmem + L::DP_COL, v_s, dout);
+                    mma_extra(tmem + L::DP_COL, ones_s, d_s + (uint32_t)(it & 1) * L::EXTRA);
+                    tc_commit(dp_full);
+                };
                 auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
                 auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
-                bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
-                if (ok) { mma_abt<DP>(tmem + L::S_COL, k_s, q_at(0)); tc_commit(s_full); }
+                bool ok = wait(kv_full, 0) && wait(&q_full[0], 0) && wait(extra_ready, 0);
+                if (ok) do_s_product(0, q_at(0));
                 ok = ok && wait(&do_full[0], 0);
-                if (ok) { mma_abt<DP>(tmem + L::DP_COL, v_s, do_at(0)); tc_commit(dp_full); }
+                if (ok) do_dp_product(0, do_at(0));
                 for (int it = 0; it < n && ok; ++it) {
                     const bool more = it + 1 < n;
                     if (!(ok = wait(p_ready, it))) break;
@@ -420,16 +454,14 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     if (more) {
                         // the next S^T takes the place of P^T: products run in order
                         if (!(ok = wait(&q_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
-                        mma_abt<DP>(tmem + L::S_COL, k_s, q_at(it + 1));
-                        tc_commit(s_full);
+                        do_s_product(it + 1, q_at(it + 1));
                     }
                     if (!(ok = wait(ds_ready, it))) break;
                     mma_halves<DP>(tmem + L::DK_COL, tmem + L::DP_COL, q_at(it), it > 0);
                     tc_commit(&q_empty[it % L::SLOTS]);
                     if (more) {
                         if (!(ok = wait(&do_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
-                        mma_abt<DP>(tmem + L::DP_COL, v_s, do_at(it + 1));
-                        tc_commit(dp_full);
+                        do_dp_product(it + 1, do_at(it + 1));
                     }
                 }
                 if (ok) tc_commit(dkv_full);
@@ -444,44 +476,63 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             const uint32_t s_t = tmem + lane_base + L::S_COL + 64u * half, dp_t = tmem + lane_base + L::DP_COL + 64u * half;
             bool ok = true;
             int tile = first, head = kv_head * p.group;
-            // thread t of half 0 fetches lse, of half 1 D, of row t of the next item
-            auto fetch = [&](int tl, int hd) {
-                const int row = tl * AT_ROWS + t;
-                if (row >= lq) return 0.f;
-                return (half == 0 ? p.lse : p.delta)[(size_t)hd * p.total_q + q0 + row];
+            // thread t of half 0 brings lse, of half 1 D, of row t of an item: fetched two items ahead,
+            // written one ahead (the item before has left the turn's columns by then)
+            int f_tile = first, f_head = head;
+            auto fetch = [&](int item) {
+                const int row = f_tile * AT_ROWS + t;
+                float v = 0.f;
+                if (item < n && row < lq) v = (half == 0 ? p.lse : p.delta)[(size_t)f_head * p.total_q + q0 + row];
+                if (++f_tile == tiles) { f_tile = first; ++f_head; }
+                return v;
             };
-            float next = n > 0 ? fetch(tile, head) : 0.f;           // (used an item later: nothing waits for it)
-            for (int it = 0; it < n; ++it) {
-                float* st = stats + (it & 1) * 256;
-                st[half * 128 + t] = half == 0 ? -AT_LOG2E * next : -next;
+            const float inv_scale = 1.f / p.scale;
+            const uint32_t extra_s = smem_u32(half == 0 ? s_lse : s_d) + extra_at(t, 0);
+            auto put = [&](int item, float v) {
+                v = half == 0 ? -v * inv_scale : -v;
+                const float hi = __bfloat162float(__float2bfloat16_rn(v));
+                const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
+                const uint32_t at = extra_s + (uint32_t)(item & 1) * L::EXTRA;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(at), "r"(bf16x2(hi, mid)),
+                             "r"(bf16x2(v - hi - mid, 0.f)) : "memory");
+            };
+            float next = 0.f;
+            if (n > 0) {
+                // columns 0-2 of the ones are 1, all others of the extra columns 0
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                for (int i = (int)threadIdx.x; i < 5 * L::EXTRA / 16; i += BW_MATH) sts128(smem_u32(smem) + 16u * i, zero);
                 math_sync();
+                if (half == 0) sts128(smem_u32(s_ones) + extra_at(t, 0), make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u));
+                put(0, fetch(0));
+                next = fetch(1);
+                fence_proxy_async_smem();
+                mbar_arrive(extra_ready);
+            }
+            for (int it = 0; it < n; ++it) {
+                if (it + 1 < n) {
+                    put(it + 1, next);
+                    fence_proxy_async_smem();       // p_ready below orders it before the products
+                    next = fetch(it + 2);
+                }
                 const int row0 = tile * AT_ROWS;
                 if (++tile == tiles) { tile = first; ++head; }
-                if (it + 1 < n) next = fetch(tile, head);
                 // query i of the tile sees this thread's key when i >= unseen; rows from lq on are none
                 const int unseen = key - shift - row0 - 64 * half, live = lq - row0 - 64 * half;
                 const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + AT_ROWS > lq;
-                const float4* lse4 = reinterpret_cast<const float4*>(st + 64 * half);
-                const float4* d4 = reinterpret_cast<const float4*>(st + 128 + 64 * half);
 
-                // a warp whose wait gave up goes on without waiting: the others meet it in math_sync
-                ok = ok && mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32];
                 load64(s_t, s);
                 uint32_t pr[32];
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
+                for (int i = 0; i < 64; i += 2) {
                     uint32_t* x = &s[i / 32][i % 32];
-                    const float4 l4 = lse4[i / 4];
                     float a, b;
-                    unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, pack2(l4.x, l4.y)), a, b);
+                    unpack2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2), a, b);
                     x[0] = __float_as_uint(ex2(a));
                     x[1] = __float_as_uint(ex2(b));
-                    unpack2(fma2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, pack2(l4.z, l4.w)), a, b);
-                    x[2] = __float_as_uint(ex2(a));
-                    x[3] = __float_as_uint(ex2(b));
                 }
                 if (edge) {
 #pragma unroll
@@ -494,8 +545,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tmem_st_32x32b_x32(s_t, pr);
                 if (row0 + AT_ROWS > lq) {
                     // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
-                    ok = ok && mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     zero_rows<DP>(smem_u32(s_do + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
                     zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
                     fence_proxy_async_smem();
@@ -504,27 +555,23 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(p_ready);
 
-                ok = ok && mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t dp[2][32];
                 load64(dp_t, dp);
-                if (edge) {         // P is 0 there, but dP - D of a row of no sequence need not be finite
+                if (edge) {         // P is 0 there, but dP - D need not be finite
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         if (i < unseen || i >= live) dp[i / 32][i % 32] = 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
+                for (int i = 0; i < 64; i += 2) {
                     const uint32_t *x = &s[i / 32][i % 32], *y = &dp[i / 32][i % 32];
-                    const float4 e4 = d4[i / 4];
                     float a, b;
                     unpack2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                 add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(e4.x, e4.y))), a, b);
+                                 pack2(__uint_as_float(y[0]), __uint_as_float(y[1]))), a, b);
                     pr[i / 2] = bf16x2(a, b);
-                    unpack2(mul2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                 add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(e4.z, e4.w))), a, b);
-                    pr[i / 2 + 1] = bf16x2(a, b);
                 }
                 tmem_st_32x32b_x32(dp_t, pr);
                 tmem_st_wait();
