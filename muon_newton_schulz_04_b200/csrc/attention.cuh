@@ -160,6 +160,16 @@ __device__ __forceinline__ void mma_abt_half(uint32_t d_tmem, uint32_t a, uint32
     }
 }
 
+// The same for quarter q, 32 rows of B.
+template <int DP>
+__device__ __forceinline__ void mma_tb_quarter(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int q, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+        tc_mma_f16_ts(d_tmem, a_tmem + 8u * kk, smem_desc_sw128(b + (uint32_t)(2 * q + kk) * 2048u, AT_CHUNK, 1024), idesc,
+                      accumulate || kk != 0);
+}
+
 // 64 fp32 columns of this thread's row.
 __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
     tmem_ld_32x32b_x32(taddr, v[0]);

@@ -63,6 +63,7 @@ struct DqLayout {
     static constexpr int BARRIERS = 2 + 2 * KS + 2 * VS + 6;
     static constexpr int SMEM = 1024 + (2 + KS + VS) * TILE + 8 * BARRIERS + 2 * 128 * 4 + 64;
     static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;        // S: two buffers of 128
+    static constexpr int ON_FMA = 2;                                        // of 8 pairs of exponentials
     static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
 };
 
@@ -245,10 +246,18 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 load64(s_t, s);
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {
+                    const uint64_t x2 =
+                        fma2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2, l2);
                     float x, y;
-                    unpack2(fma2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])), c2, l2), x, y);
-                    s[i / 32][i % 32] = __float_as_uint(ex2(x));
-                    s[i / 32][i % 32 + 1] = __float_as_uint(ex2(y));
+                    if (i / 2 % 8 < L::ON_FMA) {
+                        exp2_pair(x2, x, y);
+                    } else {
+                        unpack2(x2, x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                    }
+                    s[i / 32][i % 32] = __float_as_uint(x);
+                    s[i / 32][i % 32 + 1] = __float_as_uint(y);
                 }
                 ok = mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_BW_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -320,10 +329,11 @@ template <int DP>
 struct DkvLayout {
     static constexpr int TILE = DP / 64 * AT_CHUNK;
     static constexpr int SLOTS = DP == 64 ? 3 : 2;              // of q and of dO
-    static constexpr int BARRIERS = 2 + 4 * SLOTS + 5;
+    static constexpr int BARRIERS = 2 + 4 * SLOTS + 6;
     static constexpr int EXTRA = 128 * 16 * 2;                  // 16 more columns of a tile
     static constexpr int SMEM = 1024 + 5 * EXTRA + (2 + 2 * SLOTS) * TILE + 8 * BARRIERS + 64;
     static constexpr uint32_t S_COL = 0, DP_COL = 128, DK_COL = 256, DV_COL = 384;
+    static constexpr int ON_FMA = 2;                            // of 8 pairs of exponentials
     static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
 };
 
@@ -339,7 +349,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(s_do + L::SLOTS * L::TILE);
     uint64_t* extra_ready = kv_full + 1;        // the ones, and the first item's columns
     uint64_t *q_full = extra_ready + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
-    uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 1,
+    uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 2,
              *dkv_full = ds_ready + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkv_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -374,7 +384,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(p_ready, BW_MATH);
+        mbar_init(&p_ready[0], BW_MATH);        // the first, then the last 32 columns of both halves
+        mbar_init(&p_ready[1], BW_MATH);
         mbar_init(ds_ready, BW_MATH);
         mbar_init(dkv_full, 1);
         *abort_flag = 0;
@@ -448,8 +459,12 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 if (ok) do_dp_product(0, do_at(0));
                 for (int it = 0; it < n && ok; ++it) {
                     const bool more = it + 1 < n;
-                    if (!(ok = wait(p_ready, it))) break;
-                    mma_halves<DP>(tmem + L::DV_COL, tmem + L::S_COL, do_at(it), it > 0);
+                    for (int c = 0; c < 2 && ok; ++c) {
+                        if (!(ok = wait(&p_ready[c], it))) break;
+                        mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 16u * c, do_at(it), c, it > 0 || c > 0);
+                        mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 64u + 16u * c, do_at(it), 2 + c, true);
+                    }
+                    if (!ok) break;
                     tc_commit(&do_empty[it % L::SLOTS]);
                     if (more) {
                         // the next S^T takes the place of P^T: products run in order
@@ -525,24 +540,6 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tc_fence_after();
                 uint32_t s[2][32];
                 load64(s_t, s);
-                uint32_t pr[32];
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    uint32_t* x = &s[i / 32][i % 32];
-                    float a, b;
-                    unpack2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2), a, b);
-                    x[0] = __float_as_uint(ex2(a));
-                    x[1] = __float_as_uint(ex2(b));
-                }
-                if (edge) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i < unseen || i >= live) s[i / 32][i % 32] = 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    pr[i] = bf16x2(__uint_as_float(s[i / 16][2 * i % 32]), __uint_as_float(s[i / 16][2 * i % 32 + 1]));
-                tmem_st_32x32b_x32(s_t, pr);
                 if (row0 + AT_ROWS > lq) {
                     // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
                     ok = mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
@@ -551,14 +548,40 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
                     fence_proxy_async_smem();
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(p_ready);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const uint64_t x2 = mul2(pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2);
+                        float a, b;
+                        if (i / 2 % 8 < L::ON_FMA) {
+                            exp2_pair(x2, a, b);
+                        } else {
+                            unpack2(x2, a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                        }
+                        s[q][i] = __float_as_uint(a);
+                        s[q][i + 1] = __float_as_uint(b);
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * q + i < unseen || 32 * q + i >= live) s[q][i] = 0u;
+                    }
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) pr[i] = bf16x2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
+                    tmem_st_32x32b_x16(s_t + 16u * q, pr);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&p_ready[q]);
+                }
 
                 ok = mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t dp[2][32];
+                uint32_t dp[2][32], pr[32];
                 load64(dp_t, dp);
                 if (edge) {         // P is 0 there, but dP - D need not be finite
 #pragma unroll
