@@ -555,16 +555,16 @@ muon_status encode_sym_maps(muon_handle* h, CUtensorMap* m2, const void* base, i
                           CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Tensor map of a rows x heads array: dims (head_dim, heads, rows), boxes of 128 rows of
-// 64 columns of one head.  Strides over a single row or head are replaced by ones that
+// Tensor map of a rows x heads array: dims (head_dim, heads, rows), boxes of `box_rows` rows
+// of 64 columns of one head.  Strides over a single row or head are replaced by ones that
 // the encoder takes; an array without rows gets a map of one row that is never loaded.
 muon_status encode_heads(muon_handle* h, CUtensorMap* m, const muon_heads& v, int rows, int heads, int d,
-                         const void* no_rows) {
+                         int box_rows, const void* no_rows) {
     const void* base = rows > 0 ? v.ptr : no_rows;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)std::max(rows, 1)};
     const cuuint64_t strides[2] = {heads > 1 && rows > 0 ? (cuuint64_t)v.head_stride * 2 : 16,
                                    rows > 1 ? (cuuint64_t)v.row_stride * 2 : 16};
-    const cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, estr[3] = {1, 1, 1};
     const CUresult r = h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -573,12 +573,12 @@ muon_status encode_heads(muon_handle* h, CUtensorMap* m, const muon_heads& v, in
     return MUON_OK;
 }
 
-muon_status attention_maps(muon_handle* h, const muon_attention_args& a, HeadMaps* m) {
+muon_status attention_maps(muon_handle* h, const muon_attention_args& a, int box_rows, HeadMaps* m) {
     muon_status st = load_encoder(h);
     if (st != MUON_OK) return st;
-    if ((st = encode_heads(h, &m->q, a.q, a.total_q, a.n_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
-    if ((st = encode_heads(h, &m->k, a.k, a.total_k, a.n_kv_heads, a.head_dim, h->d_err)) != MUON_OK) return st;
-    return encode_heads(h, &m->v, a.v, a.total_k, a.n_kv_heads, a.head_dim, h->d_err);
+    if ((st = encode_heads(h, &m->q, a.q, a.total_q, a.n_heads, a.head_dim, box_rows, h->d_err)) != MUON_OK) return st;
+    if ((st = encode_heads(h, &m->k, a.k, a.total_k, a.n_kv_heads, a.head_dim, box_rows, h->d_err)) != MUON_OK) return st;
+    return encode_heads(h, &m->v, a.v, a.total_k, a.n_kv_heads, a.head_dim, box_rows, h->d_err);
 }
 
 // Tensor maps of a weight gradient's operands.
@@ -1535,7 +1535,7 @@ muon_status muon_attention(muon_handle* h, const muon_attention_args* a, void* s
     h->last_error.clear();
     NvtxRange nr("attention");
     HeadMaps maps;
-    if ((st = attention_maps(h, *a, &maps)) != MUON_OK) return st;
+    if ((st = attention_maps(h, *a, AT_FWD_BOX, &maps)) != MUON_OK) return st;
     CUDA_TRY(h, launch_attention(attention_params(h, *a), maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }
@@ -1558,8 +1558,8 @@ muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_ar
     p.dq = head_view(g->dq); p.dk = head_view(g->dk); p.dv = head_view(g->dv);
     p.delta = g->delta;
     HeadMaps maps;
-    if ((st = attention_maps(h, g->forward, &maps)) != MUON_OK) return st;
-    if ((st = encode_heads(h, &maps.go, g->grad_out, p.total_q, p.hq, p.d, h->d_err)) != MUON_OK) return st;
+    if ((st = attention_maps(h, g->forward, AT_BWD_BOX, &maps)) != MUON_OK) return st;
+    if ((st = encode_heads(h, &maps.go, g->grad_out, p.total_q, p.hq, p.d, AT_BWD_BOX, h->d_err)) != MUON_OK) return st;
     CUDA_TRY(h, launch_attention_backward(p, maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }

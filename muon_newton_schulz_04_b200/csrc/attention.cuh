@@ -117,6 +117,15 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Loads ROWS rows from `row` on of one head, DP columns, as chunks of 64 columns.
+template <int DP, int ROWS, int BOX>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+        for (int r = 0; r < ROWS; r += BOX) tma_load_3d(dst + (c * ROWS + r) * 128, map, bar, 64 * c, head, row + r);
+}
+
 // ---------------------------------------------------------------- products of tiles
 // Tiles lie in shared memory as 64-column chunks of AT_CHUNK bytes, 128-byte swizzled, one
 // 128-byte line per row.
@@ -126,19 +135,20 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo
     return smem_desc_sw128(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61);
 }
 
-// D = A * B^T over `dp` columns: A and B 128-row tiles with the contraction along their rows.
-template <int DP>
+// D = A * B^T over DP columns: A a tile of 128 rows, B one of N, contraction along the rows.
+template <int DP, int N>
 __device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b) {
-    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS, 0);
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, N, 0);
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-        const uint32_t off = (uint32_t)(kk / 4) * AT_CHUNK + (uint32_t)(kk % 4) * 32u;
-        tc_mma_f16(d_tmem, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc, kk != 0);
+        const uint32_t c = (uint32_t)(kk / 4), off = (uint32_t)(kk % 4) * 32u;
+        tc_mma_f16(d_tmem, smem_desc_sw128(a + c * AT_CHUNK + off, 16, 1024),
+                   smem_desc_sw128(b + c * (N * 128u) + off, 16, 1024), idesc, kk != 0);
     }
 }
 
-// D (+)= A_h * B_h: half h (64 of the 128 rows of B) of the contraction, A_h 128 x 64 bf16 in
-// tensor memory.
+// D (+)= A_h * B_h: rows 64 h .. 64 h + 63 of B are the contraction, A_h is 128 x 64 bf16 in
+// tensor memory, B a tile of DP columns (128 rows when it has two chunks of columns).
 template <int DP>
 __device__ __forceinline__ void mma_tb_half(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int h, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, DP, 1);
@@ -146,18 +156,6 @@ __device__ __forceinline__ void mma_tb_half(uint32_t d_tmem, uint32_t a_tmem, ui
     for (int kk = 0; kk < 4; ++kk)
         tc_mma_f16_ts(d_tmem, a_tmem + 8u * kk, smem_desc_sw128(b + (uint32_t)(4 * h + kk) * 2048u, AT_CHUNK, 1024), idesc,
                       accumulate || kk != 0);
-}
-
-// D = A * B_h^T: A a 128-row tile, B_h rows 64 h .. 64 h + 63 of one, contraction along the rows.
-template <int DP>
-__device__ __forceinline__ void mma_abt_half(uint32_t d_tmem, uint32_t a, uint32_t b, int h) {
-    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS / 2, 0);
-#pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
-        const uint32_t off = (uint32_t)(kk / 4) * AT_CHUNK + (uint32_t)(kk % 4) * 32u;
-        tc_mma_f16(d_tmem, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off + 8192u * (uint32_t)h, 16, 1024), idesc,
-                   kk != 0);
-    }
 }
 
 // The same for quarter q, 32 rows of B.
@@ -177,13 +175,14 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
     tmem_ld_wait();
 }
 
-// Zeroes rows [first, 128) of a tile of DP columns; called by `threads` threads, `t` this one's
+// Zeroes rows [first, rows) of a tile of DP columns; called by `threads` threads, `t` this one's
 // index.  The caller orders the writes before the products that read the tile.
 template <int DP>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int t, int threads) {
-    for (int i = first * 8 + t; i < AT_ROWS * 8; i += threads)
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int rows, int t, int threads) {
+    for (int i = first * 8 + t; i < rows * 8; i += threads)
 #pragma unroll
-        for (int c = 0; c < DP / 64; ++c) sts128(tile + (uint32_t)c * AT_CHUNK + (uint32_t)i * 16u, make_uint4(0, 0, 0, 0));
+        for (int c = 0; c < DP / 64; ++c)
+            sts128(tile + (uint32_t)(c * rows) * 128u + (uint32_t)i * 16u, make_uint4(0, 0, 0, 0));
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -218,12 +217,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Largest of three; NaN when one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// NaN when one of them is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -232,12 +231,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // 2^x of two values on the FMA pipe, which has time to spare beside the special function unit:
 // x = n + f with n the nearest integer (Cody-Waite), 2^f by its minimax polynomial of degree 4
-// on [-1/2, 1/2] (Remez exchange; relative error 2.6e-6), n added to the exponent.  Finite x
-// below -126 gives 2^-126, as does -inf; NaN, +inf and x >= 128 give no meaningful value.
+// on [-1/2, 1/2] (Remez exchange; relative error 2.6e-6), times 2^n.  Below -126, -inf
+// included, the result is 2^-126; NaN stays NaN, +inf gives NaN.
 __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
     float x, y;
     unpack2(x2, x, y);
-    x2 = pack2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+    x2 = pack2(max_nan(x, -126.f), max_nan(y, -126.f));
     constexpr float MAGIC = 12582912.f;         // 1.5 * 2^23: the sum's low bits are the nearest integer
     const uint64_t t2 = add2(x2, pack2(MAGIC, MAGIC));
     const uint64_t f2 = fma2(add2(t2, pack2(-MAGIC, -MAGIC)), pack2(-1.f, -1.f), x2);
@@ -245,11 +244,10 @@ __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
     p2 = fma2(p2, f2, pack2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
     p2 = fma2(p2, f2, pack2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
     p2 = fma2(p2, f2, pack2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
-    float tx, ty, px, py;
+    float tx, ty;
     unpack2(t2, tx, ty);
-    unpack2(p2, px, py);
-    a = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
-    b = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
+    unpack2(mul2(p2, pack2(__uint_as_float((__float_as_uint(tx) << 23) + 0x3F800000u),
+                           __uint_as_float((__float_as_uint(ty) << 23) + 0x3F800000u))), a, b);
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

@@ -18,8 +18,13 @@
 //
 // In both, P and dS go back to tensor memory as bf16 in the place of the fp32 tile that they
 // were formed from, and are the A operand there: only Q, K, V and dO tiles lie in shared
-// memory.  Eight warps form P and dS: warp w owns rows 32 (w % 4) .., warps 0-3 the first 64
-// columns and warps 4-7 the last.
+// memory.
+//
+// A CTA owns 128 rows and goes through the others in steps of as many as a head is wide.
+// 128-wide heads: one CTA an SM, eight warps form P and dS (warp w has rows 32 (w % 4) ..,
+// warps 0-3 the first 64 columns of a step, warps 4-7 the last).  64-wide heads: half the
+// tensor memory, so two CTAs an SM, four such warps each, which also hide each other's start
+// and end (eight sequences of 1024, 25 heads: 225 us with one CTA an SM, XX with two).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -28,43 +33,50 @@
 namespace muon {
 namespace {
 
-constexpr int BW_MATH = 256;
-constexpr int BW_THREADS = BW_MATH + 64;        // + the TMA warp and the MMA warp
-
 constexpr int ERR_BW_LOAD = 0x211, ERR_BW_MMA = 0x212, ERR_BW_MATH = 0x213;
 
-__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-// D (+)= A B: A 128 x 128 bf16 in tensor memory, its halves 64 columns apart.
+// What both kernels share.
 template <int DP>
-__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
-    mma_tb_half<DP>(d_tmem, a_tmem, b, 0, accumulate);
-    mma_tb_half<DP>(d_tmem, a_tmem + 64u, b, 1, true);
-}
+struct BwLayout {
+    static constexpr int HALVES = DP / 64;                      // of a step's columns
+    static constexpr int STEP = DP;                             // rows of a streamed tile
+    static constexpr int MATH = 128 * HALVES, THREADS = MATH + 128;     // + a warpgroup: TMA, MMA, tensor memory
+    static constexpr int W_TMA = MATH / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 2;
+    static constexpr int CTAS = 2 / HALVES;                     // of an SM
+    static constexpr int REGS = HALVES == 1 ? 128 : 168;        // a thread: at launch, then of the math warps and the others
+    static constexpr int REGS_MATH = HALVES == 1 ? 168 : 200, REGS_OTHER = HALVES == 1 ? 88 : 104;
+    static_assert(MATH * REGS_MATH + 128 * REGS_OTHER <= THREADS * REGS, "more registers than launched with");
+    static constexpr int OWN = 128 * DP * 2, MOVING = STEP * DP * 2;    // bytes of the tiles
+    static constexpr int MOST_SMEM = 232448 / CTAS - (CTAS - 1) * 1024;
+    static constexpr uint32_t TMEM_COLS = 4 * DP;
+    static constexpr int ON_FMA = 2;                            // of 8 pairs of exponentials
+};
 
-// One more K step of 16: D += A B^T of two 128 x 16 tiles without swizzle (core matrices of 8
-// rows x 16 bytes, the two of a row 2048 bytes apart, groups of 8 rows 128 bytes apart).
+template <int DP>
+__device__ __forceinline__ void math_sync() { named_sync(1, BwLayout<DP>::MATH); }
+
+// One more K step of 16: D += A B^T of tiles of 128 and N rows of 16 columns without
+// swizzle (core matrices of 8 rows x 16 bytes; groups of 8 rows 128 bytes apart, the two of a
+// row 16 bytes times the rows).
+template <int N>
 __device__ __forceinline__ void mma_extra(uint32_t d_tmem, uint32_t a, uint32_t b) {
-    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, AT_ROWS, 0);
-    tc_mma_f16(d_tmem, smem_desc_plain(a, 2048, 128), smem_desc_plain(b, 2048, 128), idesc, 1u);
+    constexpr uint32_t idesc = idesc_bf16_f32(AT_ROWS, N, 0);
+    tc_mma_f16(d_tmem, smem_desc_plain(a, 2048, 128), smem_desc_plain(b, N * 16, 128), idesc, 1u);
 }
 
-// Byte of column c of row r of such a tile.
-__device__ __forceinline__ uint32_t extra_at(int r, int c) {
-    return (uint32_t)((c >> 3) * 2048 + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2);
-}
+// Byte of the first column of row r of such a tile.
+__device__ __forceinline__ uint32_t extra_at(int r) { return (uint32_t)((r >> 3) * 128 + (r & 7) * 16); }
 
 // ============================================================================ dQ
 
 template <int DP>
-struct DqLayout {
-    static constexpr int TILE = DP / 64 * AT_CHUNK;
+struct DqLayout : BwLayout<DP> {
+    using Base = BwLayout<DP>;
     static constexpr int KS = DP == 64 ? 4 : 3, VS = DP == 64 ? 3 : 2;      // ring slots: K is used twice
     static constexpr int BARRIERS = 2 + 2 * KS + 2 * VS + 6;
-    static constexpr int SMEM = 1024 + (2 + KS + VS) * TILE + 8 * BARRIERS + 2 * 128 * 4 + 64;
-    static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;        // S: two buffers of 128
-    static constexpr int ON_FMA = 2;                                        // of 8 pairs of exponentials
-    static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
+    static constexpr int SMEM = 1024 + 2 * Base::OWN + (KS + VS) * Base::MOVING + 8 * BARRIERS + 2 * 128 * 4 + 64;
+    static constexpr uint32_t S_COL = 0, DP_COL = 2 * DP, DQ_COL = 3 * DP;  // S: two buffers
+    static_assert(SMEM <= Base::MOST_SMEM, "shared memory above the SM's 228 KiB");
 };
 
 struct BwMaps {
@@ -72,13 +84,13 @@ struct BwMaps {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(BW_THREADS, 1)
+__global__ void __launch_bounds__(BwLayout<DP>::THREADS, BwLayout<DP>::CTAS)
 attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwMaps maps) {
     using L = DqLayout<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *s_q = smem, *s_do = s_q + L::TILE, *s_k = s_do + L::TILE, *s_v = s_k + L::KS * L::TILE;
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_v + L::VS * L::TILE);
+    uint8_t *s_q = smem, *s_do = s_q + L::OWN, *s_k = s_do + L::OWN, *s_v = s_k + L::KS * L::MOVING;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_v + L::VS * L::MOVING);
     uint64_t* do_full = q_full + 1;
     uint64_t *k_full = do_full + 1, *k_empty = k_full + L::KS, *v_full = k_empty + L::KS, *v_empty = v_full + L::VS;
     uint64_t *s_full = v_empty + L::VS, *dp_full = s_full + 2, *dp_read = dp_full + 1, *ds_ready = dp_read + 1,
@@ -101,8 +113,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
             info[1] = make_int4(ok ? t.blocks - 1 - t.block : 0, 0, 0, 0);      // long rows first
         }
-    } else if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
+    } else if (warp == L::W_TMEM) {
+        tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
@@ -113,8 +125,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         mbar_init(&s_full[0], 1);                       // one per buffer: S runs a tile ahead
         mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
-        mbar_init(dp_read, BW_MATH);
-        mbar_init(ds_ready, BW_MATH);
+        mbar_init(dp_read, L::MATH);
+        mbar_init(ds_ready, L::MATH);
         mbar_init(dq_full, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -128,38 +140,36 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         const int q0 = sl.x, lq = sl.y, k0 = sl.z, lk = sl.w;
         const int row0 = info[1].x * AT_ROWS, shift = lk - lq, kv_head = head / p.group;
         const int last = min(row0 + AT_ROWS, lq) - 1 + shift;       // last key that any row sees
-        const int n = last < 0 ? 0 : last / AT_ROWS + 1;
+        const int n = last < 0 ? 0 : last / L::STEP + 1;
 
-        if (warp == 8) {
+        if (warp == L::W_TMA) {
+            regs_less<L::REGS_OTHER>();
             if (elect_one() && n > 0) {
-                mbar_arrive_expect_tx(q_full, L::TILE);
-                for (int c = 0; c < DP / 64; ++c)
-                    tma_load_3d(s_q + c * AT_CHUNK, &maps.q, q_full, 64 * c, head, q0 + row0);
+                mbar_arrive_expect_tx(q_full, L::OWN);
+                load_tile<DP, 128, AT_BWD_BOX>(s_q, &maps.q, q_full, head, q0 + row0);
                 bool ok = true;
                 for (int j = 0; j < n + L::KS; ++j) {       // the last turns only wait for the loads to be used
                     const int ks = j % L::KS, vs = j % L::VS;
                     if (!mbar_wait(&k_empty[ks], ((uint32_t)(j / L::KS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
                     if (j < n) {
-                        mbar_arrive_expect_tx(&k_full[ks], L::TILE);
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(s_k + ks * L::TILE + c * AT_CHUNK, &maps.k, &k_full[ks], 64 * c, kv_head, k0 + j * AT_ROWS);
+                        mbar_arrive_expect_tx(&k_full[ks], L::MOVING);
+                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_k + ks * L::MOVING, &maps.k, &k_full[ks], kv_head, k0 + j * L::STEP);
                     }
                     if (j == 0) {
-                        mbar_arrive_expect_tx(do_full, L::TILE);
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(s_do + c * AT_CHUNK, &maps.go, do_full, 64 * c, head, q0 + row0);
+                        mbar_arrive_expect_tx(do_full, L::OWN);
+                        load_tile<DP, 128, AT_BWD_BOX>(s_do, &maps.go, do_full, head, q0 + row0);
                     }
                     if (j < n + L::VS &&
                         !mbar_wait(&v_empty[vs], ((uint32_t)(j / L::VS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
                     if (j < n) {
-                        mbar_arrive_expect_tx(&v_full[vs], L::TILE);
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(s_v + vs * L::TILE + c * AT_CHUNK, &maps.v, &v_full[vs], 64 * c, kv_head, k0 + j * AT_ROWS);
+                        mbar_arrive_expect_tx(&v_full[vs], L::MOVING);
+                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_v + vs * L::MOVING, &maps.v, &v_full[vs], kv_head, k0 + j * L::STEP);
                     }
                 }
                 if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
-        } else if (warp == 9) {
+        } else if (warp == L::W_MMA) {
+            regs_less<L::REGS_OTHER>();
             if (elect_one() && n > 0) {
                 const uint32_t q_s = smem_u32(s_q), do_s = smem_u32(s_do), k_s = smem_u32(s_k), v_s = smem_u32(s_v);
                 auto wait = [&](uint64_t* b, int use) {
@@ -168,11 +178,11 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     return ok;
                 };
                 auto do_s_product = [&](int j) {
-                    mma_abt<DP>(tmem + L::S_COL + 128u * (j & 1), q_s, k_s + (uint32_t)(j % L::KS) * L::TILE);
+                    mma_abt<DP, L::STEP>(tmem + L::S_COL + (uint32_t)(DP * (j & 1)), q_s, k_s + (uint32_t)(j % L::KS) * L::MOVING);
                     tc_commit(&s_full[j & 1]);
                 };
                 auto do_dp_product = [&](int j) {
-                    mma_abt<DP>(tmem + L::DP_COL, do_s, v_s + (uint32_t)(j % L::VS) * L::TILE);
+                    mma_abt<DP, L::STEP>(tmem + L::DP_COL, do_s, v_s + (uint32_t)(j % L::VS) * L::MOVING);
                     tc_commit(dp_full);
                     tc_commit(&v_empty[j % L::VS]);
                 };
@@ -189,24 +199,29 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         do_dp_product(j + 1);
                     }
                     if (!(ok = wait(ds_ready, j))) break;
-                    mma_halves<DP>(tmem + L::DQ_COL, tmem + L::S_COL + 128u * (j & 1), k_s + (uint32_t)(j % L::KS) * L::TILE, j > 0);
+                    for (int h = 0; h < L::HALVES; ++h)
+                        mma_tb_half<DP>(tmem + L::DQ_COL, tmem + L::S_COL + (uint32_t)(DP * (j & 1) + 64 * h),
+                                        k_s + (uint32_t)(j % L::KS) * L::MOVING, h, j > 0 || h > 0);
                     tc_commit(&k_empty[j % L::KS]);
                 }
                 if (ok) tc_commit(dq_full);
                 if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
+        } else if (warp >= L::W_TMA) {
+            regs_less<L::REGS_OTHER>();
         } else {
+            regs_more<L::REGS_MATH>();
             const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
             const uint32_t lane_base = (warp & 3u) * 32u << 16;
             const int row = row0 + t;
             const bool live = row < lq;
             const size_t stat = (size_t)head * p.total_q + q0 + (live ? row : 0);
             const float c = p.scale * AT_LOG2E;
-            // D of the rows: a warp takes 16 of them, 16 bytes a lane, all loads in flight at once (a row per
-            // thread reads 32 lines a load: 12000 cycles)
+            // D of the rows: 16 bytes a lane, whole rows a warp, all loads in flight at once (a row per thread
+            // reads 32 lines a load: 12000 cycles)
             {
-                constexpr int LANES = DP / 8, ROWS = 32 / LANES, TURNS = 16 / ROWS;
-                const int lane = t & 31, r0 = (int)warp * 16 + lane / LANES, col = lane % LANES * 8;
+                constexpr int LANES = DP / 8, ROWS = 32 / LANES, PER_WARP = 32 / L::HALVES, TURNS = PER_WARP / ROWS;
+                const int lane = t & 31, r0 = (int)warp * PER_WARP + lane / LANES, col = lane % LANES * 8;
                 uint4 x[TURNS], y[TURNS];
 #pragma unroll
                 for (int i = 0; i < TURNS; ++i) {
@@ -231,9 +246,9 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     if (lane % LANES == 0) exch[r0 + i * ROWS] = sum;
                 }
             }
-            math_sync();
-            const float D = exch[t];
             const float lse2 = live ? p.lse[stat] * AT_LOG2E : 0.f;
+            math_sync<DP>();
+            const float D = exch[t];
             const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-D, -D);
             float rest = 0.f;                   // sum of dS: 0 but for the rounding of O in D
             bool ok = true;
@@ -241,7 +256,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 ok = mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_BW_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t s_t = tmem + lane_base + L::S_COL + 128u * (j & 1) + 64u * half;
+                const uint32_t s_t = tmem + lane_base + L::S_COL + (uint32_t)(DP * (j & 1) + 64 * half);
                 uint32_t s[2][32];
                 load64(s_t, s);
 #pragma unroll
@@ -266,8 +281,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 load64(tmem + lane_base + L::DP_COL + 64u * half, dp);
                 tc_fence_before();
                 mbar_arrive(dp_read);
-                const int seen = row + shift - j * AT_ROWS - 64 * half;     // column of the last seen key
-                const bool edge = (j + 1) * AT_ROWS > row0 + shift + 1;
+                const int seen = row + shift - j * L::STEP - 64 * half;     // column of the last seen key
+                const bool edge = (j + 1) * L::STEP > row0 + shift + 1;
                 uint32_t ds[32];
                 uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll
@@ -288,9 +303,9 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 unpack2(sum2, a, b);
                 rest += a + b;
                 tmem_st_32x32b_x32(s_t, ds);
-                if (lk - j * AT_ROWS < AT_ROWS) {
+                if (lk - j * L::STEP < L::STEP) {
                     // rows behind the sequence's keys: dS is 0 there, but 0 times what lies behind need not be
-                    zero_rows<DP>(smem_u32(s_k + (j % L::KS) * L::TILE), lk - j * AT_ROWS, (int)threadIdx.x, BW_MATH);
+                    zero_rows<DP>(smem_u32(s_k + (j % L::KS) * L::MOVING), lk - j * L::STEP, L::STEP, (int)threadIdx.x, L::MATH);
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
@@ -304,49 +319,53 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             }
             // sum_j P_ij = 1, so D + sum_j dS_ij is sum_j P_ij dP_ij without O's rounding: the
             // second kernel takes that
-            math_sync();
-            exch[half * 128 + t] = rest;
-            math_sync();
+            if (L::HALVES == 2) {
+                math_sync<DP>();
+                exch[half * 128 + t] = rest;
+                math_sync<DP>();
+                rest += exch[(half ^ 1) * 128 + t];
+            }
             if (ok) {
-                if (half == 0 && live) p.delta[stat] = D + exch[t] + exch[128 + t];
-                store_rows<DP>(tmem + lane_base + L::DQ_COL + (uint32_t)(half * (DP / 2)), n > 0, n == 0, p.scale,
-                               smem_u32(s_q), half, (int)(warp & 3u) * 32, lq - row0,
-                               p.dq.p + (long long)(q0 + row0) * p.dq.rs + (long long)head * p.dq.hs, p.dq.rs, p.d);
+                if (half == 0 && live) p.delta[stat] = D + rest;
+                for (int h = half; h < 2; h += L::HALVES)
+                    store_rows<DP>(tmem + lane_base + L::DQ_COL + (uint32_t)(h * (DP / 2)), n > 0, n == 0, p.scale,
+                                   smem_u32(s_q), h, (int)(warp & 3u) * 32, lq - row0,
+                                   p.dq.p + (long long)(q0 + row0) * p.dq.rs + (long long)head * p.dq.hs, p.dq.rs, p.d);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == L::W_TMEM) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, L::TMEM_COLS);
     }
 }
 
 // ============================================================================ dK, dV
 
 template <int DP>
-struct DkvLayout {
-    static constexpr int TILE = DP / 64 * AT_CHUNK;
+struct DkvLayout : BwLayout<DP> {
+    using Base = BwLayout<DP>;
     static constexpr int SLOTS = DP == 64 ? 3 : 2;              // of q and of dO
     static constexpr int BARRIERS = 2 + 4 * SLOTS + 6;
-    static constexpr int EXTRA = 128 * 16 * 2;                  // 16 more columns of a tile
-    static constexpr int SMEM = 1024 + 5 * EXTRA + (2 + 2 * SLOTS) * TILE + 8 * BARRIERS + 64;
-    static constexpr uint32_t S_COL = 0, DP_COL = 128, DK_COL = 256, DV_COL = 384;
-    static constexpr int ON_FMA = 2;                            // of 8 pairs of exponentials
-    static_assert(SMEM <= 232448, "shared memory above the 227 KiB limit");
+    static constexpr int ONES = 128 * 16 * 2, EXTRA = Base::STEP * 16 * 2;      // 16 more columns of the tiles
+    static constexpr int SMEM = 1024 + ONES + 4 * EXTRA + 2 * Base::OWN + 2 * SLOTS * Base::MOVING + 8 * BARRIERS + 64;
+    static constexpr uint32_t S_COL = 0, DP_COL = DP, DK_COL = 2 * DP, DV_COL = 3 * DP;
+    static_assert(SMEM <= Base::MOST_SMEM, "shared memory above the SM's 228 KiB");
+    static_assert((ONES + 4 * EXTRA) % 1024 == 0, "the tiles behind the extra columns start a swizzle atom");
 };
 
 template <int DP>
-__global__ void __launch_bounds__(BW_THREADS, 1)
+__global__ void __launch_bounds__(BwLayout<DP>::THREADS, BwLayout<DP>::CTAS)
 attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwMaps maps) {
     using L = DkvLayout<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // the extra columns: ones beside K and V, two turns of those beside Q and beside dO
-    uint8_t *s_ones = smem, *s_lse = s_ones + L::EXTRA, *s_d = s_lse + 2 * L::EXTRA;
-    uint8_t *s_k = smem + 5 * L::EXTRA, *s_v = s_k + L::TILE, *s_q = s_v + L::TILE, *s_do = s_q + L::SLOTS * L::TILE;
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(s_do + L::SLOTS * L::TILE);
+    uint8_t *s_ones = smem, *s_lse = s_ones + L::ONES, *s_d = s_lse + 2 * L::EXTRA;
+    uint8_t *s_k = s_d + 2 * L::EXTRA, *s_v = s_k + L::OWN, *s_q = s_v + L::OWN, *s_do = s_q + L::SLOTS * L::MOVING;
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(s_do + L::SLOTS * L::MOVING);
     uint64_t* extra_ready = kv_full + 1;        // the ones, and the first item's columns
     uint64_t *q_full = extra_ready + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
     uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 2,
@@ -369,13 +388,13 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
             info[1] = make_int4(t.block, 0, 0, 0);
         }
-    } else if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
+    } else if (warp == L::W_TMEM) {
+        tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
         mbar_init(kv_full, 1);
-        mbar_init(extra_ready, BW_MATH);
+        mbar_init(extra_ready, L::MATH);
         for (int i = 0; i < L::SLOTS; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -384,9 +403,9 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(&p_ready[0], BW_MATH);        // the first, then the last 32 columns of both halves
-        mbar_init(&p_ready[1], BW_MATH);
-        mbar_init(ds_ready, BW_MATH);
+        mbar_init(&p_ready[0], L::MATH);        // the first, then the last 32 columns of both halves
+        mbar_init(&p_ready[1], L::MATH);
+        mbar_init(ds_ready, L::MATH);
         mbar_init(dkv_full, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -399,17 +418,16 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         const int4 sl = info[0];
         const int q0 = sl.x, lq = sl.y, k0 = sl.z, lk = sl.w;
         const int key0 = info[1].x * AT_ROWS, shift = lk - lq;
-        const int tiles = (lq + AT_ROWS - 1) / AT_ROWS, first = max(0, key0 - shift) / AT_ROWS;   // query tiles that see any of the keys
+        const int tiles = (lq + L::STEP - 1) / L::STEP, first = max(0, key0 - shift) / L::STEP;   // query tiles that see any of the keys
         const int per_head = max(0, tiles - first), n = per_head * p.group;
         // item `it`: query tile first + it % per_head of head kv_head * group + it / per_head
 
-        if (warp == 8) {
+        if (warp == L::W_TMA) {
+            regs_less<L::REGS_OTHER>();
             if (elect_one() && n > 0) {
-                mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
-                for (int c = 0; c < DP / 64; ++c) {
-                    tma_load_3d(s_k + c * AT_CHUNK, &maps.k, kv_full, 64 * c, kv_head, k0 + key0);
-                    tma_load_3d(s_v + c * AT_CHUNK, &maps.v, kv_full, 64 * c, kv_head, k0 + key0);
-                }
+                mbar_arrive_expect_tx(kv_full, 2 * L::OWN);
+                load_tile<DP, 128, AT_BWD_BOX>(s_k, &maps.k, kv_full, kv_head, k0 + key0);
+                load_tile<DP, 128, AT_BWD_BOX>(s_v, &maps.v, kv_full, kv_head, k0 + key0);
                 bool ok = true;
                 int tile = first, head = kv_head * p.group;
                 for (int it = 0; it < n + L::SLOTS; ++it) {     // the last turns only wait for the loads to be used
@@ -417,21 +435,20 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     const uint32_t par = ((uint32_t)(it / L::SLOTS) & 1u) ^ 1u;
                     if (!mbar_wait(&q_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
                     if (it < n) {
-                        mbar_arrive_expect_tx(&q_full[slot], L::TILE);
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(s_q + slot * L::TILE + c * AT_CHUNK, &maps.q, &q_full[slot], 64 * c, head, q0 + tile * AT_ROWS);
+                        mbar_arrive_expect_tx(&q_full[slot], L::MOVING);
+                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_q + slot * L::MOVING, &maps.q, &q_full[slot], head, q0 + tile * L::STEP);
                     }
                     if (!mbar_wait(&do_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
                     if (it < n) {
-                        mbar_arrive_expect_tx(&do_full[slot], L::TILE);
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(s_do + slot * L::TILE + c * AT_CHUNK, &maps.go, &do_full[slot], 64 * c, head, q0 + tile * AT_ROWS);
+                        mbar_arrive_expect_tx(&do_full[slot], L::MOVING);
+                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_do + slot * L::MOVING, &maps.go, &do_full[slot], head, q0 + tile * L::STEP);
                     }
                     if (++tile == tiles) { tile = first; ++head; }
                 }
                 if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
-        } else if (warp == 9) {
+        } else if (warp == L::W_MMA) {
+            regs_less<L::REGS_OTHER>();
             if (elect_one() && n > 0) {
                 const uint32_t k_s = smem_u32(s_k), v_s = smem_u32(s_v), q_s = smem_u32(s_q), do_s = smem_u32(s_do);
                 auto wait = [&](uint64_t* b, int use) {
@@ -442,17 +459,17 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 // S^T - lse / scale and dP^T - D
                 const uint32_t ones_s = smem_u32(s_ones), lse_s = smem_u32(s_lse), d_s = smem_u32(s_d);
                 auto do_s_product = [&](int it, uint32_t q) {
-                    mma_abt<DP>(tmem + L::S_COL, k_s, q);
-                    mma_extra(tmem + L::S_COL, ones_s, lse_s + (uint32_t)(it & 1) * L::EXTRA);
+                    mma_abt<DP, L::STEP>(tmem + L::S_COL, k_s, q);
+                    mma_extra<L::STEP>(tmem + L::S_COL, ones_s, lse_s + (uint32_t)(it & 1) * L::EXTRA);
                     tc_commit(s_full);
                 };
                 auto do_dp_product = [&](int it, uint32_t dout) {
-                    mma_abt<DP>(tmem + L::DP_COL, v_s, dout);
-                    mma_extra(tmem + L::DP_COL, ones_s, d_s + (uint32_t)(it & 1) * L::EXTRA);
+                    mma_abt<DP, L::STEP>(tmem + L::DP_COL, v_s, dout);
+                    mma_extra<L::STEP>(tmem + L::DP_COL, ones_s, d_s + (uint32_t)(it & 1) * L::EXTRA);
                     tc_commit(dp_full);
                 };
-                auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
-                auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::TILE; };
+                auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
+                auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
                 bool ok = wait(kv_full, 0) && wait(&q_full[0], 0) && wait(extra_ready, 0);
                 if (ok) do_s_product(0, q_at(0));
                 ok = ok && wait(&do_full[0], 0);
@@ -461,8 +478,9 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     const bool more = it + 1 < n;
                     for (int c = 0; c < 2 && ok; ++c) {
                         if (!(ok = wait(&p_ready[c], it))) break;
-                        mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 16u * c, do_at(it), c, it > 0 || c > 0);
-                        mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 64u + 16u * c, do_at(it), 2 + c, true);
+                        for (int h = 0; h < L::HALVES; ++h)
+                            mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 64u * h + 16u * c, do_at(it), 2 * h + c,
+                                               it > 0 || c > 0 || h > 0);
                     }
                     if (!ok) break;
                     tc_commit(&do_empty[it % L::SLOTS]);
@@ -472,7 +490,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                         do_s_product(it + 1, q_at(it + 1));
                     }
                     if (!(ok = wait(ds_ready, it))) break;
-                    mma_halves<DP>(tmem + L::DK_COL, tmem + L::DP_COL, q_at(it), it > 0);
+                    for (int h = 0; h < L::HALVES; ++h)
+                        mma_tb_half<DP>(tmem + L::DK_COL, tmem + L::DP_COL + 64u * h, q_at(it), h, it > 0 || h > 0);
                     tc_commit(&q_empty[it % L::SLOTS]);
                     if (more) {
                         if (!(ok = wait(&do_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
@@ -482,7 +501,10 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 if (ok) tc_commit(dkv_full);
                 if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
+        } else if (warp >= L::W_TMA) {
+            regs_less<L::REGS_OTHER>();
         } else {
+            regs_more<L::REGS_MATH>();
             const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
             const uint32_t lane_base = (warp & 3u) * 32u << 16;
             const int key = key0 + t;
@@ -491,20 +513,22 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             const uint32_t s_t = tmem + lane_base + L::S_COL + 64u * half, dp_t = tmem + lane_base + L::DP_COL + 64u * half;
             bool ok = true;
             int tile = first, head = kv_head * p.group;
-            // thread t of half 0 brings lse, of half 1 D, of row t of an item: fetched two items ahead,
-            // written one ahead (the item before has left the turn's columns by then)
+            // the first half of the threads brings lse, the other one D, of a row of an item each: fetched two
+            // items ahead, written one ahead (the item before has left the turn's columns by then)
+            const bool brings_d = (int)threadIdx.x >= L::STEP;
+            const int brings = (int)threadIdx.x % L::STEP;
             int f_tile = first, f_head = head;
             auto fetch = [&](int item) {
-                const int row = f_tile * AT_ROWS + t;
+                const int row = f_tile * L::STEP + brings;
                 float v = 0.f;
-                if (item < n && row < lq) v = (half == 0 ? p.lse : p.delta)[(size_t)f_head * p.total_q + q0 + row];
+                if (item < n && row < lq) v = (brings_d ? p.delta : p.lse)[(size_t)f_head * p.total_q + q0 + row];
                 if (++f_tile == tiles) { f_tile = first; ++f_head; }
                 return v;
             };
             const float inv_scale = 1.f / p.scale;
-            const uint32_t extra_s = smem_u32(half == 0 ? s_lse : s_d) + extra_at(t, 0);
+            const uint32_t extra_s = smem_u32(brings_d ? s_d : s_lse) + extra_at(brings);
             auto put = [&](int item, float v) {
-                v = half == 0 ? -v * inv_scale : -v;
+                v = brings_d ? -v : -v * inv_scale;
                 const float hi = __bfloat162float(__float2bfloat16_rn(v));
                 const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
                 const uint32_t at = extra_s + (uint32_t)(item & 1) * L::EXTRA;
@@ -515,9 +539,9 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             if (n > 0) {
                 // columns 0-2 of the ones are 1, all others of the extra columns 0
                 const uint4 zero = make_uint4(0, 0, 0, 0);
-                for (int i = (int)threadIdx.x; i < 5 * L::EXTRA / 16; i += BW_MATH) sts128(smem_u32(smem) + 16u * i, zero);
-                math_sync();
-                if (half == 0) sts128(smem_u32(s_ones) + extra_at(t, 0), make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u));
+                for (int i = (int)threadIdx.x; i < (L::ONES + 4 * L::EXTRA) / 16; i += L::MATH) sts128(smem_u32(smem) + 16u * i, zero);
+                math_sync<DP>();
+                if (half == 0) sts128(smem_u32(s_ones) + extra_at(t), make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u));
                 put(0, fetch(0));
                 next = fetch(1);
                 fence_proxy_async_smem();
@@ -529,23 +553,23 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     fence_proxy_async_smem();       // p_ready below orders it before the products
                     next = fetch(it + 2);
                 }
-                const int row0 = tile * AT_ROWS;
+                const int row0 = tile * L::STEP;
                 if (++tile == tiles) { tile = first; ++head; }
                 // query i of the tile sees this thread's key when i >= unseen; rows from lq on are none
                 const int unseen = key - shift - row0 - 64 * half, live = lq - row0 - 64 * half;
-                const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + AT_ROWS > lq;
+                const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + L::STEP > lq;
 
                 ok = mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32];
                 load64(s_t, s);
-                if (row0 + AT_ROWS > lq) {
+                if (row0 + L::STEP > lq) {
                     // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
                     ok = mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    zero_rows<DP>(smem_u32(s_do + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
-                    zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::TILE), lq - row0, (int)threadIdx.x, BW_MATH);
+                    zero_rows<DP>(smem_u32(s_do + (it % L::SLOTS) * L::MOVING), lq - row0, L::STEP, (int)threadIdx.x, L::MATH);
+                    zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::MOVING), lq - row0, L::STEP, (int)threadIdx.x, L::MATH);
                     fence_proxy_async_smem();
                 }
 #pragma unroll
@@ -607,21 +631,23 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 tc_fence_after();
             }
             if (ok) {
-                const uint32_t col = (uint32_t)(half * (DP / 2));
-                store_rows<DP>(tmem + lane_base + L::DK_COL + col, n > 0, n == 0, p.scale, smem_u32(s_k), half,
-                               (int)(warp & 3u) * 32, lk - key0,
-                               p.dk.p + (long long)(k0 + key0) * p.dk.rs + (long long)kv_head * p.dk.hs, p.dk.rs, p.d);
-                store_rows<DP>(tmem + lane_base + L::DV_COL + col, n > 0, n == 0, 1.f, smem_u32(s_v), half,
-                               (int)(warp & 3u) * 32, lk - key0,
-                               p.dv.p + (long long)(k0 + key0) * p.dv.rs + (long long)kv_head * p.dv.hs, p.dv.rs, p.d);
+                for (int h = half; h < 2; h += L::HALVES) {
+                    const uint32_t col = (uint32_t)(h * (DP / 2));
+                    store_rows<DP>(tmem + lane_base + L::DK_COL + col, n > 0, n == 0, p.scale, smem_u32(s_k), h,
+                                   (int)(warp & 3u) * 32, lk - key0,
+                                   p.dk.p + (long long)(k0 + key0) * p.dk.rs + (long long)kv_head * p.dk.hs, p.dk.rs, p.d);
+                    store_rows<DP>(tmem + lane_base + L::DV_COL + col, n > 0, n == 0, 1.f, smem_u32(s_v), h,
+                                   (int)(warp & 3u) * 32, lk - key0,
+                                   p.dv.p + (long long)(k0 + key0) * p.dv.rs + (long long)kv_head * p.dv.hs, p.dv.rs, p.d);
+                }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == L::W_TMEM) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, L::TMEM_COLS);
     }
 }
 
@@ -630,22 +656,25 @@ unsigned most_tiles(int total, int n_seqs) { return (unsigned)(total / AT_ROWS +
 
 template <int DP>
 cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) {
+    using L = BwLayout<DP>;
     cudaError_t e;
+    if ((e = cudaFuncSetAttribute(attention_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<DP>::SMEM)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(attention_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvLayout<DP>::SMEM)) != cudaSuccess) return e;
+    // a warpgroup that asks for more registers than the launch left would wait for good
+    static const int regs = [] {
+        cudaFuncAttributes a, b;
+        return cudaFuncGetAttributes(&a, attention_dq_kernel<DP>) == cudaSuccess &&
+               cudaFuncGetAttributes(&b, attention_dkv_kernel<DP>) == cudaSuccess ? std::min(a.numRegs, b.numRegs) : 0;
+    }();
+    if (regs < L::REGS) return cudaErrorInvalidConfiguration;
     if (p.total_q > 0) {
-        e = cudaFuncSetAttribute(attention_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<DP>::SMEM);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(attention_dq_kernel<DP>, dim3(most_tiles(p.total_q, p.n_seqs) * (unsigned)p.hq), dim3(BW_THREADS),
+        e = launch_pdl(attention_dq_kernel<DP>, dim3(most_tiles(p.total_q, p.n_seqs) * (unsigned)p.hq), dim3(L::THREADS),
                        DqLayout<DP>::SMEM, s, p, maps);
         if (e != cudaSuccess) return e;
     }
-    if (p.total_k > 0) {
-        e = cudaFuncSetAttribute(attention_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvLayout<DP>::SMEM);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(attention_dkv_kernel<DP>, dim3(most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk), dim3(BW_THREADS),
-                       DkvLayout<DP>::SMEM, s, p, maps);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if (p.total_k == 0) return cudaSuccess;
+    return launch_pdl(attention_dkv_kernel<DP>, dim3(most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk), dim3(L::THREADS),
+                      DkvLayout<DP>::SMEM, s, p, maps);
 }
 
 }  // namespace

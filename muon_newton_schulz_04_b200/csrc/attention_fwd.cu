@@ -37,7 +37,7 @@ struct FwLayout {
     static constexpr int W_TMA = SOFTMAX / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 3;
     // registers a thread: at launch, then of the softmax warpgroups and the other one
     static constexpr int REGS = TILES == 1 ? 128 : 168;
-    static constexpr int REGS_SOFTMAX = TILES == 1 ? 216 : 232, REGS_OTHER = 40;
+    static constexpr int REGS_SOFTMAX = TILES == 1 ? 200 : 216, REGS_OTHER = TILES == 1 ? 56 : 72;
     static_assert(SOFTMAX * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS, "more registers than launched with");
     static constexpr int TILE = DP / 64 * AT_CHUNK;                 // bytes of a q, k or v tile
     static constexpr int SLOTS = 5;                                 // ring of k and v tiles
@@ -151,9 +151,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             if (elect_one() && nmax > 0) {
                 mbar_arrive_expect_tx(q_full, TILES * L::TILE);
                 for (int w = 0; w < TILES; ++w)
-                    for (int c = 0; c < DP / 64; ++c)
-                        tma_load_3d(sq + w * L::TILE + c * AT_CHUNK, &maps.q, q_full, 64 * c, head,
-                                    q0 + row0 + w * AT_ROWS);
+                    load_tile<DP, AT_ROWS, AT_ROWS>(sq + w * L::TILE, &maps.q, q_full, head, q0 + row0 + w * AT_ROWS);
                 // ring order: K0, K1, V0, K2, V1, ...: the order of use
                 int slot = 0;
                 uint32_t phase = 0;
@@ -163,9 +161,8 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     const int j = i == 0 ? 0 : is_v ? (i == 2 * nmax - 1 ? nmax - 1 : i / 2 - 1) : (i + 1) / 2;
                     if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err, ERR_FW_LOAD)) { ok = false; break; }
                     mbar_arrive_expect_tx(&full[slot], L::TILE);
-                    for (int c = 0; c < DP / 64; ++c)
-                        tma_load_3d(ring + slot * L::TILE + c * AT_CHUNK, is_v ? &maps.v : &maps.k, &full[slot], 64 * c,
-                                    kv_head, k0 + j * AT_ROWS);
+                    load_tile<DP, AT_ROWS, AT_ROWS>(ring + slot * L::TILE, is_v ? &maps.v : &maps.k, &full[slot], kv_head,
+                                                    k0 + j * AT_ROWS);
                     if (++slot == L::SLOTS) { slot = 0; phase ^= 1u; }
                 }
                 // every load has landed before the CTA may end
@@ -193,7 +190,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 auto do_s = [&](int j) {
                     if (!wait_full(k_at(j))) return false;
                     tc_fence_after();
-                    mma_abt<DP>(s_t, q_s, tile_s(k_at(j)));
+                    mma_abt<DP, AT_ROWS>(s_t, q_s, tile_s(k_at(j)));
                     tc_commit(&s_full[w]);
                     tc_commit(&empty[k_at(j) % L::SLOTS]);
                     return true;
@@ -240,7 +237,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             const int all_see = row0 + w * AT_ROWS + shift + 1;     // keys that all rows see
             float m = -INFINITY, top = -INFINITY;                   // scaled by; true maximum
             float l = 0.f;
-            bool ok = true, bad = false;                            // bad: a NaN among the logits
+            bool ok = true;
             const int nw = n[w];
             auto wait = [&](uint64_t* bar, int use) {
                 ok = ok && mbar_wait(bar, (uint32_t)use & 1u, abort_flag, p.err, ERR_FW_SOFTMAX);
@@ -269,16 +266,15 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 }
                 float x8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x8[e] = max_nan(__uint_as_float(s[0][2 * e]), __uint_as_float(s[0][2 * e + 1]));
+                for (int e = 0; e < 8; ++e) x8[e] = fmaxf(__uint_as_float(s[0][2 * e]), __uint_as_float(s[0][2 * e + 1]));
 #pragma unroll
                 for (int i = 16; i < 128; i += 16)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        x8[e] = max3_nan(x8[e], __uint_as_float(s[i / 32][i % 32 + 2 * e]),
-                                         __uint_as_float(s[i / 32][i % 32 + 2 * e + 1]));
-                const float mx = max3_nan(max3_nan(x8[0], x8[1], x8[2]), max3_nan(x8[3], x8[4], x8[5]), max_nan(x8[6], x8[7]));
-                bad = bad || mx != mx;
-                top = fmaxf(top, mx);
+                        x8[e] = max3(x8[e], __uint_as_float(s[i / 32][i % 32 + 2 * e]),
+                                     __uint_as_float(s[i / 32][i % 32 + 2 * e + 1]));
+                // (a NaN among the logits is passed over here, and makes the sum NaN)
+                top = max3(max3(top, x8[0], x8[1]), max3(x8[2], x8[3], x8[4]), max3(x8[5], x8[6], x8[7]));
                 const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * c > 8.f;
                 if (L::P_APART && j > 0) {                          // the P before has been read
                     wait(&pv_done[w], j - 1);
@@ -304,7 +300,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     // rows behind the sequence's keys: P is 0 there, but 0 times what lies behind need not be
                     const int at = j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2;
                     wait(&full[at % L::SLOTS], at / L::SLOTS);
-                    zero_rows<DP>(smem_u32(ring + (at % L::SLOTS) * L::TILE), lk - key0, t, 128);
+                    zero_rows<DP>(smem_u32(ring + (at % L::SLOTS) * L::TILE), lk - key0, AT_ROWS, t, 128);
                     fence_proxy_async_smem();
                 }
                 const float base = m == -INFINITY ? 0.f : m * c;
@@ -340,7 +336,6 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 unpack2(add2(sum2[0], sum2[1]), a, b);
                 l += a + b;
             }
-            if (bad || m == INFINITY) l = __uint_as_float(0x7FC00000u);
             if (ok && nmax > 0) {
                 // q's tile is written over: its products, or without any its load, are done
                 ok = mbar_wait(nw > 0 ? &o_full[w] : q_full, 0, abort_flag, p.err, ERR_FW_SOFTMAX);

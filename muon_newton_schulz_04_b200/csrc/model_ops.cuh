@@ -33,8 +33,9 @@ struct AttnParams {
 // device error word: a sequence whose cu_seqlens are out of range
 constexpr int ERR_SEQLENS = 0x301;
 
-// Tensor maps over [rows][heads][head_dim] arrays, boxes of 128 rows x 64 columns of one
-// head, 128-byte swizzle, zeros outside (go: backward only).
+// Tensor maps over [rows][heads][head_dim] arrays, boxes of AT_FWD_BOX or AT_BWD_BOX rows x
+// 64 columns of one head, 128-byte swizzle, zeros outside (go: backward only).
+constexpr int AT_FWD_BOX = 128, AT_BWD_BOX = 64;
 struct HeadMaps {
     CUtensorMap q, k, v, go;
 };
