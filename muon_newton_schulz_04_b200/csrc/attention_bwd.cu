@@ -248,13 +248,15 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             }
             const float lse2 = live ? p.lse[stat] * AT_LOG2E : 0.f;
             math_sync<DP>();
-            const float D = exch[t];
-            const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-D, -D);
+            float D = exch[t];
+            const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2);
             float rest = 0.f;                   // sum of dS: 0 but for the rounding of O in D
             bool ok = true;
             for (int j = 0; j < n; ++j) {
+                // (with one step the warps meet in barriers: one whose wait gave up goes on without waiting)
                 ok = mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_BW_MATH);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok && n > 1) break;
                 tc_fence_after();
                 const uint32_t s_t = tmem + lane_base + L::S_COL + (uint32_t)(DP * (j & 1) + 64 * half);
                 uint32_t s[2][32];
@@ -274,8 +276,9 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     s[i / 32][i % 32] = __float_as_uint(x);
                     s[i / 32][i % 32 + 1] = __float_as_uint(y);
                 }
-                ok = mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_BW_MATH);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = ok && mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok && n > 1) break;
                 tc_fence_after();
                 uint32_t dp[2][32];
                 load64(tmem + lane_base + L::DP_COL + 64u * half, dp);
@@ -283,6 +286,26 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 mbar_arrive(dp_read);
                 const int seen = row + shift - j * L::STEP - 64 * half;     // column of the last seen key
                 const bool edge = (j + 1) * L::STEP > row0 + shift + 1;
+                if (n == 1) {
+                    // few keys: O's rounding in D is not small beside dP, and D = sum_j P_ij dP_ij is at hand
+                    uint64_t d4[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+                    float x, y;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        unpack2(mul2(pack2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1])),
+                                     pack2(__uint_as_float(dp[i / 32][i % 32]), __uint_as_float(dp[i / 32][i % 32 + 1]))), x, y);
+                        d4[i / 2 & 1] = add2(d4[i / 2 & 1], pack2(i > seen ? 0.f : x, i + 1 > seen ? 0.f : y));
+                    }
+                    unpack2(add2(d4[0], d4[1]), x, y);
+                    D = x + y;
+                    if (L::HALVES == 2) {
+                        math_sync<DP>();
+                        exch[half * 128 + t] = D;
+                        math_sync<DP>();
+                        D += exch[(half ^ 1) * 128 + t];
+                    }
+                }
+                const uint64_t d2 = pack2(-D, -D);
                 uint32_t ds[32];
                 uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll
