@@ -103,8 +103,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 
     const uint32_t warp = warp_id();
     const int head = (int)(blockIdx.x % (unsigned)p.hq);
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();          // after the wait: the second kernel starts on what came before this one
     if (warp == 0) {
         SeqTile t;
         const bool ok = find_tile(p, false, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x == 0, t);
@@ -401,7 +401,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     const uint32_t warp = warp_id();
     const int kv_head = (int)(blockIdx.x % (unsigned)p.hk);
     pdl_trigger();
-    pdl_wait();
+    // No wait here: of the first kernel's work only D is read, below, and that kernel let this one
+    // start when all work before it was done.
     if (warp == 0) {
         SeqTile t;
         // first blocks of a sequence first: most queries see them
@@ -559,6 +560,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                              "r"(bf16x2(v - hi - mid, 0.f)) : "memory");
             };
             float next = 0.f;
+            pdl_wait();                             // D is there
             if (n > 0) {
                 // columns 0-2 of the ones are 1, all others of the extra columns 0
                 const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -666,6 +668,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             }
         }
     }
+    pdl_wait();             // whatever this CTA had to do: the grid ends after the first kernel's
     tc_fence_before();
     __syncthreads();
     if (warp == L::W_TMEM) {
@@ -696,6 +699,12 @@ cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) 
         if (e != cudaSuccess) return e;
     }
     if (p.total_k == 0) return cudaSuccess;
+    // (without queries the kernel before is another one's, and its CTAs wait for nothing they read: cu_seqlens
+    // and the zeros they write come after a plain launch)
+    if (p.total_q == 0) {
+        attention_dkv_kernel<DP><<<most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk, L::THREADS, DkvLayout<DP>::SMEM, s>>>(p, maps);
+        return cudaGetLastError();
+    }
     return launch_pdl(attention_dkv_kernel<DP>, dim3(most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk), dim3(L::THREADS),
                       DkvLayout<DP>::SMEM, s, p, maps);
 }

@@ -8,8 +8,8 @@
 // x / unit is exact, so a code has one rounding.
 //
 // Bound by memory: store reads 2 or 4 bytes and writes 33/32 a value, load the reverse.
-// Four lanes share a block (8 values each), so a warp covers 256 consecutive values of a
-// row with 16-byte accesses.
+// Two lanes share a block (16 values each), so codes move 16 bytes a lane, and a thread has
+// two such pieces in flight.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -20,7 +20,8 @@ namespace muon {
 namespace {
 
 constexpr int CK_THREADS = 256;
-constexpr int CK_VALS = 8;          // values of one thread
+constexpr int CK_VALS = 16;         // values of a piece: half a block
+constexpr int CK_PIECES = 2;        // pieces of a thread in flight
 
 // 2^n for -149 <= n <= 127
 __device__ __forceinline__ float pow2f(int n) {
@@ -28,20 +29,24 @@ __device__ __forceinline__ float pow2f(int n) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* x, int n, bool vec, float (&v)[CK_VALS]) {
+__device__ __forceinline__ void load_values(const T* x, int n, bool vec, float (&v)[CK_VALS]) {
     if (vec && n >= CK_VALS) {
-        if (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4*>(x);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        constexpr int WORDS = CK_VALS * sizeof(T) / 16;
+        uint4 w[WORDS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(u[i] << 16);
-                v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint4*>(x)[i];
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(T) == 2) {
+                    v[(8 * i + 2 * e) % CK_VALS] = __uint_as_float(u[e] << 16);
+                    v[(8 * i + 2 * e + 1) % CK_VALS] = __uint_as_float(u[e] & 0xFFFF0000u);
+                } else {
+                    v[(4 * i + e) % CK_VALS] = __uint_as_float(u[e]);
+                }
             }
-        } else {
-            const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
         return;
     }
@@ -49,88 +54,135 @@ __device__ __forceinline__ void load8(const T* x, int n, bool vec, float (&v)[CK
     for (int i = 0; i < CK_VALS; ++i) v[i] = i < n ? (float)x[i] : 0.f;
 }
 
-template <typename T>
+// Piece u of rows of per_row pieces: its row and first column.  I: an index type that holds
+// the number of pieces (a 64-bit division costs as much as the rest).
+template <typename I>
+__device__ __forceinline__ void piece_at(I u, int per_row, size_t& row, int& col) {
+    const I r = u / (I)per_row;
+    row = (size_t)r;
+    col = (int)(u - r * (I)per_row) * CK_VALS;
+}
+
+template <typename T, typename I>
 __global__ void __launch_bounds__(CK_THREADS) ckpt_store_kernel(const T* __restrict__ x, int cols, long long xs, int ld,
-                                                                size_t total, int vec, int8_t* __restrict__ codes,
+                                                                I total, int vec, int8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
     pdl_trigger();
     pdl_wait();
-    // total = rows * ld / 8 eighths of blocks, a multiple of 4: the lanes of a block stay together
-    const size_t stride = (size_t)gridDim.x * CK_THREADS;
-    for (size_t u = (size_t)blockIdx.x * CK_THREADS + threadIdx.x; u < total; u += stride) {
-        const int per_row = ld / CK_VALS;
-        const size_t row = u / per_row;
-        const int c = (int)(u - row * per_row) * CK_VALS;
-        float v[CK_VALS];
-        load8(x + row * xs + c, cols - c, vec != 0, v);
-        uint32_t top = 0;               // bits of |x| order like |x|, with infinities and NaN above
+    // total = rows * ld / 16 is even and pieces of a thread are a multiple of 32 apart: the lanes
+    // of a block stay together
+    const I stride = (I)gridDim.x * CK_THREADS;
+    for (I u0 = (I)blockIdx.x * CK_THREADS + threadIdx.x; u0 < total; u0 += CK_PIECES * stride) {
+        float v[CK_PIECES][CK_VALS];
+        size_t row[CK_PIECES];
+        int col[CK_PIECES];
 #pragma unroll
-        for (int i = 0; i < CK_VALS; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        const unsigned quad = 0xFu << (threadIdx.x & 28);
-        top = max(top, __shfl_xor_sync(quad, top, 1));
-        top = max(top, __shfl_xor_sync(quad, top, 2));
-        uint32_t E;
-        if (top >= 0x7F800000u) E = 255;
-        else if (top >= 0x00800000u) E = min((top + 0x10000u) >> 23, 254u);
-        else E = (top + 0x8000u) >> 23;     // subnormal: unit 2^-133 holds all but the last binary 1/256
-        uint32_t w[2] = {0, 0};
-        if (E != 255u) {
-            // 1 / unit = 2^(133 - E) in two exact factors
-            const int n = 133 - (int)E;
-            const float f0 = pow2f(n / 2), f1 = pow2f(n - n / 2);
-#pragma unroll
-            for (int i = 0; i < CK_VALS; ++i) {
-                const int q = max(-127, min(127, __float2int_rn(v[i] * f0 * f1)));
-                w[i / 4] |= (uint32_t)(q & 0xFF) << (8 * (i % 4));
-            }
+        for (int p = 0; p < CK_PIECES; ++p) {
+            const I u = u0 + p * stride;
+            if (u >= total) continue;
+            piece_at<I>(u, ld / CK_VALS, row[p], col[p]);
+            load_values(x + row[p] * xs + col[p], cols - col[p], vec != 0, v[p]);
         }
-        *reinterpret_cast<uint2*>(codes + row * ld + c) = make_uint2(w[0], w[1]);
-        if ((threadIdx.x & 3) == 0) scales[row * (ld / CKPT_BLOCK) + c / CKPT_BLOCK] = (uint8_t)E;
+#pragma unroll
+        for (int p = 0; p < CK_PIECES; ++p) {
+            if (u0 + p * stride >= total) continue;
+            uint32_t top = 0;               // bits of |x| order like |x|, with infinities and NaN above
+#pragma unroll
+            for (int i = 0; i < CK_VALS; ++i) top = max(top, __float_as_uint(v[p][i]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+            uint32_t E;
+            if (top >= 0x7F800000u) E = 255;
+            // k = exponent field - 127: unit 2^(k-6) is E = k + 127
+            else if (top >= 0x00800000u) E = min((top + 0x10000u) >> 23, 254u);
+            else E = (top + 0x8000u) >> 23;     // subnormal: unit 2^-133 holds all but the last binary 1/256
+            uint32_t w[CK_VALS / 4] = {};
+            if (E != 255u) {
+                // 1 / unit = 2^(133 - E) in two exact factors
+                const int n = 133 - (int)E;
+                const float f0 = pow2f(n / 2), f1 = pow2f(n - n / 2);
+#pragma unroll
+                for (int i = 0; i < CK_VALS; ++i) {
+                    const int q = max(-127, min(127, __float2int_rn(v[p][i] * f0 * f1)));
+                    w[i / 4] |= (uint32_t)(q & 0xFF) << (8 * (i % 4));
+                }
+            }
+            *reinterpret_cast<uint4*>(codes + row[p] * ld + col[p]) = make_uint4(w[0], w[1], w[2], w[3]);
+            if ((threadIdx.x & 1) == 0) scales[row[p] * (ld / CKPT_BLOCK) + col[p] / CKPT_BLOCK] = (uint8_t)E;
+        }
     }
 }
 
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int cols, int ld,
-                                                               size_t total, T* __restrict__ x, long long xs, int vec) {
+                                                               I total, T* __restrict__ x, long long xs, int vec) {
     pdl_trigger();
     pdl_wait();
-    const size_t stride = (size_t)gridDim.x * CK_THREADS;
-    for (size_t u = (size_t)blockIdx.x * CK_THREADS + threadIdx.x; u < total; u += stride) {
-        const int per_row = ld / CK_VALS;
-        const size_t row = u / per_row;
-        const int c = (int)(u - row * per_row) * CK_VALS;
-        if (c >= cols) continue;
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + row * ld + c);
-        const uint32_t E = scales[row * (ld / CKPT_BLOCK) + c / CKPT_BLOCK];
-        const float unit = E == 255u ? __uint_as_float(0x7FC00000u) : pow2f((int)E - 133);
-        float v[CK_VALS];
+    const I stride = (I)gridDim.x * CK_THREADS;
+    for (I u0 = (I)blockIdx.x * CK_THREADS + threadIdx.x; u0 < total; u0 += CK_PIECES * stride) {
+        uint4 w4[CK_PIECES];
+        uint32_t E[CK_PIECES];
+        size_t row[CK_PIECES];
+        int col[CK_PIECES];
 #pragma unroll
-        for (int i = 0; i < CK_VALS; ++i)
-            v[i] = (float)(int8_t)((i < 4 ? w.x : w.y) >> (8 * (i % 4))) * unit;
-        T* o = x + row * xs + c;
-        if (vec && c + CK_VALS <= cols) {
-            if (sizeof(T) == 2) {
-                uint32_t b[4];
+        for (int p = 0; p < CK_PIECES; ++p) {
+            const I u = u0 + p * stride;
+            if (u >= total) continue;
+            piece_at<I>(u, ld / CK_VALS, row[p], col[p]);
+            w4[p] = *reinterpret_cast<const uint4*>(codes + row[p] * ld + col[p]);
+            E[p] = scales[row[p] * (ld / CKPT_BLOCK) + col[p] / CKPT_BLOCK];
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    b[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int p = 0; p < CK_PIECES; ++p) {
+            if (u0 + p * stride >= total || col[p] >= cols) continue;
+            const float unit = E[p] == 255u ? __uint_as_float(0x7FC00000u) : pow2f((int)E[p] - 133);
+            const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
+            float v[CK_VALS];
+#pragma unroll
+            for (int i = 0; i < CK_VALS; ++i) v[i] = (float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * unit;
+            T* o = x + row[p] * xs + col[p];
+            if (vec && col[p] + CK_VALS <= cols) {
+#pragma unroll
+                for (int i = 0; i < CK_VALS * (int)sizeof(T) / 16; ++i) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (sizeof(T) == 2) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[(8 * i + 2 * e) % CK_VALS], v[(8 * i + 2 * e + 1) % CK_VALS]);
+                            b[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        } else {
+                            b[e] = __float_as_uint(v[(4 * i + e) % CK_VALS]);
+                        }
+                    }
+                    reinterpret_cast<uint4*>(o)[i] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                *reinterpret_cast<uint4*>(o) = make_uint4(b[0], b[1], b[2], b[3]);
             } else {
-                reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                for (int i = 0; i < CK_VALS; ++i)
+                    if (col[p] + i < cols) o[i] = (T)v[i];
             }
-        } else {
-            for (int i = 0; i < CK_VALS && c + i < cols; ++i) o[i] = (T)v[i];
         }
     }
+}
+
+template <typename T, typename I>
+cudaError_t store(const T* x, int cols, long long xs, int ld, size_t total, int vec, int8_t* codes, uint8_t* scales, int grid,
+                  cudaStream_t s) {
+    return launch_pdl(ckpt_store_kernel<T, I>, dim3(grid), dim3(CK_THREADS), 0, s, x, cols, xs, ld, (I)total, vec, codes, scales);
+}
+
+template <typename T, typename I>
+cudaError_t load(const int8_t* codes, const uint8_t* scales, int cols, int ld, size_t total, T* x, long long xs, int vec,
+                 int grid, cudaStream_t s) {
+    return launch_pdl(ckpt_load_kernel<T, I>, dim3(grid), dim3(CK_THREADS), 0, s, codes, scales, cols, ld, (I)total, x, xs, vec);
 }
 
 int ckpt_grid(size_t total, int num_sms) {
-    return (int)std::min<size_t>((total + CK_THREADS - 1) / CK_THREADS, (size_t)num_sms * 16);
+    return (int)std::min<size_t>((total + CK_THREADS - 1) / CK_THREADS, (size_t)num_sms * 8);
 }
+
+// 32-bit indexes while the last of a thread's pieces stays below 2^32
+bool small_index(size_t total, int grid) { return total + (size_t)CK_PIECES * grid * CK_THREADS < (1ull << 32); }
 
 }  // namespace
 
@@ -138,24 +190,28 @@ cudaError_t launch_checkpoint_store(const void* x, int x_bf16, int rows, int col
                                     uint8_t* scales, int num_sms, cudaStream_t s) {
     const int ld = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
     const size_t total = (size_t)rows * (ld / CK_VALS);
-    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0;
-    const dim3 g(ckpt_grid(total, num_sms)), b(CK_THREADS);
-    return x_bf16 ? launch_pdl(ckpt_store_kernel<__nv_bfloat16>, g, b, 0, s, static_cast<const __nv_bfloat16*>(x), cols,
-                               xs, ld, total, vec, codes, scales)
-                  : launch_pdl(ckpt_store_kernel<float>, g, b, 0, s, static_cast<const float*>(x), cols, xs, ld, total,
-                               vec, codes, scales);
+    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0, grid = ckpt_grid(total, num_sms);
+    const auto* h = static_cast<const __nv_bfloat16*>(x);
+    const auto* f = static_cast<const float*>(x);
+    if (small_index(total, grid))
+        return x_bf16 ? store<__nv_bfloat16, uint32_t>(h, cols, xs, ld, total, vec, codes, scales, grid, s)
+                      : store<float, uint32_t>(f, cols, xs, ld, total, vec, codes, scales, grid, s);
+    return x_bf16 ? store<__nv_bfloat16, size_t>(h, cols, xs, ld, total, vec, codes, scales, grid, s)
+                  : store<float, size_t>(f, cols, xs, ld, total, vec, codes, scales, grid, s);
 }
 
 cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* scales, int rows, int cols, void* x, int x_bf16,
                                    long long xs, int num_sms, cudaStream_t s) {
     const int ld = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
     const size_t total = (size_t)rows * (ld / CK_VALS);
-    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0;
-    const dim3 g(ckpt_grid(total, num_sms)), b(CK_THREADS);
-    return x_bf16 ? launch_pdl(ckpt_load_kernel<__nv_bfloat16>, g, b, 0, s, codes, scales, cols, ld, total,
-                               static_cast<__nv_bfloat16*>(x), xs, vec)
-                  : launch_pdl(ckpt_load_kernel<float>, g, b, 0, s, codes, scales, cols, ld, total,
-                               static_cast<float*>(x), xs, vec);
+    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0, grid = ckpt_grid(total, num_sms);
+    auto* h = static_cast<__nv_bfloat16*>(x);
+    auto* f = static_cast<float*>(x);
+    if (small_index(total, grid))
+        return x_bf16 ? load<__nv_bfloat16, uint32_t>(codes, scales, cols, ld, total, h, xs, vec, grid, s)
+                      : load<float, uint32_t>(codes, scales, cols, ld, total, f, xs, vec, grid, s);
+    return x_bf16 ? load<__nv_bfloat16, size_t>(codes, scales, cols, ld, total, h, xs, vec, grid, s)
+                  : load<float, size_t>(codes, scales, cols, ld, total, f, xs, vec, grid, s);
 }
 
 }  // namespace muon
