@@ -12,6 +12,7 @@
 // two such pieces in flight.
 #include <algorithm>
 
+#include "ckpt_format.cuh"
 #include "kernels.cuh"
 #include "model_ops.cuh"
 #include "ptx.cuh"
@@ -97,14 +98,20 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_store_kernel(const T* __restr
             else E = (top + 0x8000u) >> 23;     // subnormal: unit 2^-133 holds all but the last binary 1/256
             uint32_t w[CK_VALS / 4] = {};
             if (E != 255u) {
-                // 1 / unit = 2^(133 - E) in two exact factors
+                // 1 / unit = 2^(133 - E) in two exact factors; adding 1.5 * 2^23 rounds to the nearest even
+                // integer and leaves it in the low byte (a conversion runs at a quarter of the rate)
                 const int n = 133 - (int)E;
                 const float f0 = pow2f(n / 2), f1 = pow2f(n - n / 2);
+                if (E == 254u) {            // the largest unit: codes saturate
 #pragma unroll
-                for (int i = 0; i < CK_VALS; ++i) {
-                    const int q = max(-127, min(127, __float2int_rn(v[p][i] * f0 * f1)));
-                    w[i / 4] |= (uint32_t)(q & 0xFF) << (8 * (i % 4));
+                    for (int i = 0; i < CK_VALS; ++i) v[p][i] = fminf(fmaxf(v[p][i], -127.f / f0 / f1), 127.f / f0 / f1);
                 }
+                uint32_t q[CK_VALS];
+#pragma unroll
+                for (int i = 0; i < CK_VALS; ++i) q[i] = __float_as_uint(fmaf(v[p][i] * f0, f1, 12582912.f));
+#pragma unroll
+                for (int i = 0; i < CK_VALS; i += 4)
+                    w[i / 4] = __byte_perm(__byte_perm(q[i], q[i + 1], 0x0040), __byte_perm(q[i + 2], q[i + 3], 0x0040), 0x5410);
             }
             *reinterpret_cast<uint4*>(codes + row[p] * ld + col[p]) = make_uint4(w[0], w[1], w[2], w[3]);
             if ((threadIdx.x & 1) == 0) scales[row[p] * (ld / CKPT_BLOCK) + col[p] / CKPT_BLOCK] = (uint8_t)E;
@@ -135,31 +142,41 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __r
 #pragma unroll
         for (int p = 0; p < CK_PIECES; ++p) {
             if (u0 + p * stride >= total || col[p] >= cols) continue;
-            const float unit = E[p] == 255u ? __uint_as_float(0x7FC00000u) : pow2f((int)E[p] - 133);
             const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
-            float v[CK_VALS];
-#pragma unroll
-            for (int i = 0; i < CK_VALS; ++i) v[i] = (float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * unit;
             T* o = x + row[p] * xs + col[p];
-            if (vec && col[p] + CK_VALS <= cols) {
+            // (no integer conversions: they run at a quarter of the rate)
+            if (sizeof(T) == 2) {
+                const uint32_t pair = unit_bf16(E[p]) * 0x10001u;
+                const __nv_bfloat162 unit = *reinterpret_cast<const __nv_bfloat162*>(&pair);
+                uint32_t b[CK_VALS / 2];
 #pragma unroll
-                for (int i = 0; i < CK_VALS * (int)sizeof(T) / 16; ++i) {
-                    uint32_t b[4];
+                for (int i = 0; i < CK_VALS / 2; ++i)
+                    b[i] = codes_to_bf16(__byte_perm(w[i / 2], 0, i % 2 ? 0x4342 : 0x4140), unit);
+                if (vec && col[p] + CK_VALS <= cols) {
+                    reinterpret_cast<uint4*>(o)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                    reinterpret_cast<uint4*>(o)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (sizeof(T) == 2) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[(8 * i + 2 * e) % CK_VALS], v[(8 * i + 2 * e + 1) % CK_VALS]);
-                            b[e] = *reinterpret_cast<const uint32_t*>(&h);
-                        } else {
-                            b[e] = __float_as_uint(v[(4 * i + e) % CK_VALS]);
-                        }
-                    }
-                    reinterpret_cast<uint4*>(o)[i] = make_uint4(b[0], b[1], b[2], b[3]);
+                    for (int i = 0; i < CK_VALS; ++i)
+                        if (col[p] + i < cols) reinterpret_cast<uint16_t*>(o)[i] = (uint16_t)(b[i / 2] >> (16 * (i % 2)));
                 }
             } else {
+                // 2^23 + (code + 128) is a float's bit pattern
+                const float unit = E[p] == 255u ? __uint_as_float(0x7FC00000u) : pow2f((int)E[p] - 133);
+                uint32_t b[CK_VALS];
 #pragma unroll
                 for (int i = 0; i < CK_VALS; ++i)
-                    if (col[p] + i < cols) o[i] = (T)v[i];
+                    b[i] = __float_as_uint((__uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540 + i % 4)) -
+                                            8388736.f) * unit);
+                if (vec && col[p] + CK_VALS <= cols) {
+#pragma unroll
+                    for (int i = 0; i < CK_VALS; i += 4)
+                        reinterpret_cast<uint4*>(o)[i / 4] = make_uint4(b[i], b[i + 1], b[i + 2], b[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < CK_VALS; ++i)
+                        if (col[p] + i < cols) reinterpret_cast<uint32_t*>(o)[i] = b[i];
+                }
             }
         }
     }
