@@ -97,7 +97,7 @@ __device__ __forceinline__ void convert_block(uint32_t src, uint32_t line, uint3
 // Arrives on a barrier of either CTA of the pair.  What the barrier orders lies in this CTA's
 // own shared memory and is read there by this SM's tensor core, so release at CTA scope is
 // enough, after the proxy fence; at cluster scope every stage would wait for a fence of all
-// memory (8191 tokens into 4096 x 4096: 418 us instead of 
+// memory (8191 tokens into 4096 x 4096: 418 us instead of 245).
 __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
@@ -296,18 +296,21 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
             const int in_tile = (int)rank * 128 + (int)warp * 32 + lane;
             const int row = u.tile / p.tiles_n * WG_TILE + in_tile, col0 = u.tile % p.tiles_n * WG_TILE;
             const uint32_t t_acc = tmem + acc * 256u + (warp * 32u << 16);
-            float* part = u.slot >= 0 ? p.partial + ((size_t)u.slot * WG_TILE + in_tile) * WG_TILE : nullptr;
+            // partial sums lie as 32 x 32 blocks, each as eight groups of four columns: a store of the warp
+            // covers 512 bytes (a row per lane: 32 lines a store)
+            float4* part = u.slot >= 0 ? reinterpret_cast<float4*>(p.partial) +
+                                             ((size_t)u.slot * 8 + in_tile / 32) * (WG_TILE * 8) + lane : nullptr;
 #pragma unroll 1
             for (int c = 0; c < WG_TILE / 32 && col0 + 32 * c < p.cols; ++c) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(t_acc + 32u * c, v);
                 tmem_ld_wait();
-                if (row >= p.rows) continue;
                 if (part != nullptr) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        reinterpret_cast<uint4*>(part + 32 * c)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                } else {
+                        part[c * 256 + e * 32] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                                             __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                } else if (row < p.rows) {
                     store_run(p, row, col0 + 32 * c, v);
                 }
             }
@@ -324,23 +327,16 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
     }
 }
 
-// Adds the partial sums of the split tiles in order, four columns a thread.
-__global__ void __launch_bounds__(256) weight_grad_join_kernel(const WgradParams p) {
-    pdl_trigger();
-    pdl_wait();
-    const int tile = p.whole + (int)blockIdx.y;
-    const int r = (int)blockIdx.x * 4 + (int)threadIdx.x / 64, c = (int)(threadIdx.x & 63u) * 4;
-    const int row = tile / p.tiles_n * WG_TILE + r, col = tile % p.tiles_n * WG_TILE + c;
-    if (row >= p.rows || col >= p.cols) return;
-    const float* src = p.partial + ((size_t)blockIdx.y * p.splits * WG_TILE + r) * WG_TILE + c;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < p.splits; ++k) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * WG_TILE * WG_TILE));
-        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-    }
+// Four values of one row of G.
+__device__ __forceinline__ void store_four(const WgradParams& p, int row, int col, float4 s) {
     const float v[4] = {s.x, s.y, s.z, s.w};
     const size_t at = (size_t)row * p.cols + col;
+    if (p.vec && !p.g_bf16) {
+        float4* g = reinterpret_cast<float4*>(static_cast<float*>(p.g) + at);
+        const float4 old = p.accumulate ? *g : make_float4(0.f, 0.f, 0.f, 0.f);
+        *g = make_float4(s.x + old.x, s.y + old.y, s.z + old.z, s.w + old.w);
+        return;
+    }
     for (int e = 0; e < 4 && col + e < p.cols; ++e) {
         if (p.g_bf16) {
             __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.g) + at + e;
@@ -350,6 +346,33 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const WgradParams
             *g = v[e] + (p.accumulate ? *g : 0.f);
         }
     }
+}
+
+// Adds the partial sums of a split tile's 32 x 32 block in order and writes its rows.
+__global__ void __launch_bounds__(256) weight_grad_join_kernel(const WgradParams p) {
+    __shared__ float block[32][33];
+    pdl_trigger();
+    pdl_wait();
+    const int tile = p.whole + (int)blockIdx.y, rb = (int)blockIdx.x / 8, cb = (int)blockIdx.x % 8;
+    const int row0 = tile / p.tiles_n * WG_TILE + 32 * rb, col0 = tile % p.tiles_n * WG_TILE + 32 * cb;
+    if (row0 >= p.rows || col0 >= p.cols) return;
+    const int e = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
+    const float4* src = reinterpret_cast<const float4*>(p.partial) +
+                        ((size_t)blockIdx.y * p.splits * 8 + rb) * (WG_TILE * 8) + cb * 256 + e * 32 + lane;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < p.splits; ++k) {
+        const float4 x = __ldcg(src + (size_t)k * (WG_TILE * WG_TILE / 4));
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    block[lane][4 * e] = s.x;
+    block[lane][4 * e + 1] = s.y;
+    block[lane][4 * e + 2] = s.z;
+    block[lane][4 * e + 3] = s.w;
+    __syncthreads();
+    const int r = (int)threadIdx.x / 8, c = (int)threadIdx.x % 8 * 4;
+    if (row0 + r < p.rows && col0 + c < p.cols)
+        store_four(p, row0 + r, col0 + c, make_float4(block[r][c], block[r][c + 1], block[r][c + 2], block[r][c + 3]));
 }
 
 // dy with rows that TMA cannot read (an odd address or stride), copied to rows of a multiple
@@ -406,7 +429,7 @@ cudaError_t launch_weight_grad(const WgradParams& p, const WgradMaps& maps, cuda
     const int clusters = p.whole > 0 ? WG_CLUSTERS : p.rest * p.splits;
     e = launch_pdl(weight_grad_kernel, dim3(2 * clusters), dim3(WG_THREADS), WG_SMEM, s, p, maps);
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_pdl(weight_grad_join_kernel, dim3(WG_TILE / 4, p.rest), dim3(256), 0, s, p);
+    return launch_pdl(weight_grad_join_kernel, dim3(64, p.rest), dim3(256), 0, s, p);
 }
 
 }  // namespace muon
