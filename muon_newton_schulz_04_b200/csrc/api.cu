@@ -1505,7 +1505,8 @@ muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const flo
     if (!Wq || !Wk || !max_logits) return fail(h, MUON_ERR_INVALID, "Wq, Wk and max_logits are required");
     if (n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || cols <= 0) return fail(h, MUON_ERR_INVALID, "sizes must be > 0");
     if (n_heads % n_kv_heads != 0) return fail(h, MUON_ERR_INVALID, "n_heads must be a multiple of n_kv_heads");
-    if ((long long)n_heads * head_dim > (1ll << 29) || (long long)n_heads * head_dim * cols > (1ll << 31) - 1)
+    if (n_heads + n_kv_heads > 65535) return fail(h, MUON_ERR_UNSUPPORTED, "at most 65535 heads");
+    if ((long long)n_heads * head_dim > (1ll << 31) - 1 || (long long)n_heads * head_dim * cols > (1ll << 31) - 1)
         return fail(h, MUON_ERR_INVALID, "matrix too large");
     if (!(finite(tau) && tau > 0.f)) return fail(h, MUON_ERR_INVALID, "tau must be finite and > 0");
     if (!aligned(Wq, 4) || !aligned(Wk, 4) || !aligned(max_logits, 4)) return fail(h, MUON_ERR_INVALID, "misaligned pointer");
@@ -1516,7 +1517,7 @@ muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const flo
     if (check_extents(e, 3, &why) != MUON_OK) return fail(h, MUON_ERR_INVALID, "%s", why.c_str());
     DeviceGuard dg(h->device);
     h->last_error.clear();
-    CUDA_TRY(h, launch_qk_clip_grouped(Wq, Wk, max_logits, n_heads, n_kv_heads, head_dim, cols, tau, h->num_sms,
+    CUDA_TRY(h, launch_qk_clip_grouped(Wq, Wk, max_logits, n_heads, n_kv_heads, head_dim, cols, tau,
                                        static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }

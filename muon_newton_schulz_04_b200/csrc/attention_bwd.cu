@@ -284,7 +284,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 load64(tmem + lane_base + L::DP_COL + 64u * half, dp);
                 tc_fence_before();
                 mbar_arrive(dp_read);
-                const int seen = row + shift - j * L::STEP - 64 * half;     // column of the last seen key
+                // column of the last seen key; a row that sees one key has P = 1 and dS = 0, exactly
+                const int seen = row + shift == 0 ? -1 : row + shift - j * L::STEP - 64 * half;
                 const bool edge = (j + 1) * L::STEP > row0 + shift + 1;
                 if (n == 1) {
                     // few keys: O's rounding in D is not small beside dP, and D = sum_j P_ij dP_ij is at hand
@@ -633,9 +634,11 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 uint32_t dp[2][32], pr[32];
                 load64(dp_t, dp);
                 if (edge) {         // P is 0 there, but dP - D need not be finite
+                    // (the first query that sees key 0 sees no other: its P is 1 and dS 0, exactly)
+                    const int first_ds = key == 0 ? unseen + 1 : unseen;
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
-                        if (i < unseen || i >= live) dp[i / 32][i % 32] = 0u;
+                        if (i < first_ds || i >= live) dp[i / 32][i % 32] = 0u;
                 }
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {

@@ -8,7 +8,8 @@
 // x / unit is exact, so a code has one rounding.
 //
 // Bound by memory: store reads 2 or 4 bytes and writes 33/32 a value, load the reverse.
-// Two lanes share a block (16 values each), so codes move 16 bytes a lane.  16384 x 4096 bf16
+// Two lanes share a block (16 values each), so codes move 16 bytes a lane; where the rows of x
+// do not start on 16-byte addresses, a warp takes blocks, one value of each a lane.  16384 x 4096 bf16
 // on one B200: written in 33 us, read back in 34 (201 MB each, 6.1 and 5.9 TB/s of the 6.56
 // TB/s of a copy).  What it took: no integer conversion (a quarter of the rate), no 64-bit
 // division, maxima two bf16 at a time.
@@ -35,9 +36,9 @@ template <typename T>
 struct Values {
     uint32_t w[CK_VALS * sizeof(T) / 4];
 
-    __device__ __forceinline__ void load(const T* x, int n, bool vec) {
+    __device__ __forceinline__ void load(const T* x, int n) {
         constexpr int WORDS = CK_VALS * sizeof(T) / 4;
-        if (vec && n >= CK_VALS) {
+        if (n >= CK_VALS) {
             uint4 q[WORDS / 4];
 #pragma unroll
             for (int i = 0; i < WORDS / 4; ++i) q[i] = reinterpret_cast<const uint4*>(x)[i];
@@ -86,9 +87,17 @@ __device__ __forceinline__ void piece_at(I u, int per_row, size_t& row, int& col
     col = (int)(u - r * (I)per_row) * CK_VALS;
 }
 
+// E of a block whose largest magnitude has the fp32 bits `top`.
+__device__ __forceinline__ uint32_t scale_of(uint32_t top) {
+    if (top >= 0x7F800000u) return 255u;
+    // k = exponent field - 127: unit 2^(k-6) is E = k + 127
+    if (top >= 0x00800000u) return min((top + 0x10000u) >> 23, 254u);
+    return (top + 0x8000u) >> 23;           // subnormal: unit 2^-133 holds all but the last binary 1/256
+}
+
 template <typename T, typename I>
 __global__ void __launch_bounds__(CK_THREADS) ckpt_store_kernel(const T* __restrict__ x, int cols, long long xs, int ld,
-                                                                I total, int vec, int8_t* __restrict__ codes,
+                                                                I total, int8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
     pdl_trigger();
     pdl_wait();
@@ -100,14 +109,10 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_store_kernel(const T* __restr
         int col;
         piece_at<I>(u, ld / CK_VALS, row, col);
         Values<T> v;
-        v.load(x + row * xs + col, cols - col, vec != 0);
+        v.load(x + row * xs + col, cols - col);
         uint32_t top = v.top();
         top = max(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
-        uint32_t E;
-        if (top >= 0x7F800000u) E = 255;
-        // k = exponent field - 127: unit 2^(k-6) is E = k + 127
-        else if (top >= 0x00800000u) E = min((top + 0x10000u) >> 23, 254u);
-        else E = (top + 0x8000u) >> 23;     // subnormal: unit 2^-133 holds all but the last binary 1/256
+        const uint32_t E = scale_of(top);
         uint32_t w[CK_VALS / 4] = {};
         if (E != 255u) {
             // x / unit = x * 2^(133 - E) is exact; adding 1.5 * 2^23 rounds it to the nearest even integer
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_store_kernel(const T* __restr
 template <typename T, typename I>
 __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int cols, int ld,
-                                                               I total, T* __restrict__ x, long long xs, int vec) {
+                                                               I total, T* __restrict__ x, long long xs) {
     pdl_trigger();
     pdl_wait();
     const I stride = (I)gridDim.x * CK_THREADS;
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __r
 #pragma unroll
             for (int i = 0; i < CK_VALS / 2; ++i)
                 b[i] = codes_to_bf16(__byte_perm(w[i / 2], 0, i % 2 ? 0x4342 : 0x4140), unit);
-            if (vec && col + CK_VALS <= cols) {
+            if (col + CK_VALS <= cols) {
                 reinterpret_cast<uint4*>(o)[0] = make_uint4(b[0], b[1], b[2], b[3]);
                 reinterpret_cast<uint4*>(o)[1] = make_uint4(b[4], b[5], b[6], b[7]);
             } else {
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __r
             for (int i = 0; i < CK_VALS; ++i)
                 b[i] = __float_as_uint((__uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540 + i % 4)) -
                                         8388736.f) * unit);
-            if (vec && col + CK_VALS <= cols) {
+            if (col + CK_VALS <= cols) {
 #pragma unroll
                 for (int i = 0; i < CK_VALS; i += 4)
                     reinterpret_cast<uint4*>(o)[i / 4] = make_uint4(b[i], b[i + 1], b[i + 2], b[i + 3]);
@@ -186,53 +191,132 @@ __global__ void __launch_bounds__(CK_THREADS) ckpt_load_kernel(const int8_t* __r
     }
 }
 
-template <typename T, typename I>
-cudaError_t store(const T* x, int cols, long long xs, int ld, size_t total, int vec, int8_t* codes, uint8_t* scales, int grid,
-                  cudaStream_t s) {
-    return launch_pdl(ckpt_store_kernel<T, I>, dim3(grid), dim3(CK_THREADS), 0, s, x, cols, xs, ld, (I)total, vec, codes, scales);
-}
+// Rows at any address: a warp takes a run of CK_RUN blocks of a row, a value of each a lane,
+// all of them in flight.
+constexpr int CK_RUN = 8;
+
+__device__ __forceinline__ float read_value(const __nv_bfloat16* x) { return __bfloat162float(*x); }
+__device__ __forceinline__ float read_value(const float* x) { return *x; }
 
 template <typename T, typename I>
-cudaError_t load(const int8_t* codes, const uint8_t* scales, int cols, int ld, size_t total, T* x, long long xs, int vec,
-                 int grid, cudaStream_t s) {
-    return launch_pdl(ckpt_load_kernel<T, I>, dim3(grid), dim3(CK_THREADS), 0, s, codes, scales, cols, ld, (I)total, x, xs, vec);
+__global__ void __launch_bounds__(CK_THREADS) ckpt_store_ragged_kernel(const T* __restrict__ x, int cols, long long xs, int ld,
+                                                                       I total, int8_t* __restrict__ codes,
+                                                                       uint8_t* __restrict__ scales) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = (int)(threadIdx.x & 31u), blocks = ld / CKPT_BLOCK, per_row = (blocks + CK_RUN - 1) / CK_RUN;
+    const I stride = (I)gridDim.x * (CK_THREADS / 32);
+    for (I u = (I)blockIdx.x * (CK_THREADS / 32) + threadIdx.x / 32; u < total; u += stride) {
+        const I row = u / (I)per_row;
+        const int block0 = (int)(u - row * (I)per_row) * CK_RUN, n = min(CK_RUN, blocks - block0);
+        const int col = block0 * CKPT_BLOCK + lane;
+        const T* src = x + (size_t)row * xs + col;
+        float v[CK_RUN];
+#pragma unroll
+        for (int p = 0; p < CK_RUN; ++p) v[p] = col + 32 * p < cols ? read_value(src + 32 * p) : 0.f;
+        int8_t* out = codes + (size_t)row * ld + col;
+        uint32_t mine = 0;                      // lane p keeps the scale of block p
+#pragma unroll
+        for (int p = 0; p < CK_RUN; ++p) {
+            if (p >= n) break;
+            const uint32_t E = scale_of(__reduce_max_sync(0xffffffffu, __float_as_uint(v[p]) & 0x7FFFFFFFu));
+            float q;                            // as in ckpt_store_kernel
+            if (E >= 6u && E < 254u) {
+                q = fmaf(v[p], pow2f(133 - (int)E), 12582912.f);
+            } else {
+                const int e = 133 - (int)E;
+                q = fminf(fmaxf(v[p] * pow2f(e / 2) * pow2f(e - e / 2), -127.f), 127.f) + 12582912.f;
+            }
+            out[32 * p] = E == 255u ? (int8_t)0 : (int8_t)(__float_as_uint(q) & 0xFFu);
+            if (lane == p) mine = E;
+        }
+        if (lane < n) scales[(size_t)row * blocks + block0 + lane] = (uint8_t)mine;
+    }
 }
 
-int ckpt_grid(size_t total, int num_sms) {
-    return (int)std::min<size_t>((total + CK_THREADS - 1) / CK_THREADS, (size_t)num_sms * 64);
+__device__ __forceinline__ void write_value(__nv_bfloat16* x, float v) { *x = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void write_value(float* x, float v) { *x = v; }
+
+template <typename T, typename I>
+__global__ void __launch_bounds__(CK_THREADS) ckpt_load_ragged_kernel(const int8_t* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales, int cols, int ld,
+                                                                      I total, T* __restrict__ x, long long xs) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = (int)(threadIdx.x & 31u), blocks = ld / CKPT_BLOCK, per_row = (blocks + CK_RUN - 1) / CK_RUN;
+    const I stride = (I)gridDim.x * (CK_THREADS / 32);
+    for (I u = (I)blockIdx.x * (CK_THREADS / 32) + threadIdx.x / 32; u < total; u += stride) {
+        const I row = u / (I)per_row;
+        const int block0 = (int)(u - row * (I)per_row) * CK_RUN, n = min(CK_RUN, blocks - block0);
+        const int col = block0 * CKPT_BLOCK + lane;
+        const int8_t* src = codes + (size_t)row * ld + col;
+        const uint32_t mine = lane < n ? scales[(size_t)row * blocks + block0 + lane] : 0u;     // of block `lane`
+        int c[CK_RUN];
+#pragma unroll
+        for (int p = 0; p < CK_RUN; ++p) c[p] = p < n ? src[32 * p] : 0;
+        const float unit = mine == 255u ? __uint_as_float(0x7FC00000u) : pow2f((int)mine - 133);
+        T* out = x + (size_t)row * xs + col;
+#pragma unroll
+        for (int p = 0; p < CK_RUN; ++p) {
+            const float v = (float)c[p] * __shfl_sync(0xffffffffu, unit, p);
+            if (col + 32 * p < cols) write_value(out + 32 * p, v);
+        }
+    }
 }
 
-// 32-bit indexes while a thread's index, one stride past the end, stays below 2^32
-bool small_index(size_t total, int grid) { return total + (size_t)grid * CK_THREADS < (1ull << 32); }
+struct Launch {
+    bool vec, small;        // rows on 16-byte addresses; 32-bit indexes hold every index of the loop, one stride past the end included
+    size_t total;           // pieces (vec) or runs
+    int ld;
+    dim3 grid;
+};
+
+template <typename T>
+Launch plan(const T* x, int rows, int cols, long long xs, int num_sms) {
+    Launch l;
+    l.ld = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
+    l.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (int)(16 / sizeof(T)) == 0;
+    const size_t per_block = l.vec ? CK_THREADS : CK_THREADS / 32;
+    l.total = (size_t)rows * (l.vec ? l.ld / CK_VALS : (l.ld / CKPT_BLOCK + CK_RUN - 1) / CK_RUN);
+    l.grid = dim3((unsigned)std::min<size_t>((l.total + per_block - 1) / per_block, (size_t)num_sms * 64));
+    l.small = l.total + l.grid.x * per_block < (1ull << 32);
+    return l;
+}
+
+template <typename T>
+cudaError_t store(const T* x, int rows, int cols, long long xs, int8_t* codes, uint8_t* scales, int num_sms, cudaStream_t s) {
+    const Launch l = plan(x, rows, cols, xs, num_sms);
+    const dim3 b(CK_THREADS);
+    if (l.vec)
+        return l.small ? launch_pdl(ckpt_store_kernel<T, uint32_t>, l.grid, b, 0, s, x, cols, xs, l.ld, (uint32_t)l.total, codes, scales)
+                       : launch_pdl(ckpt_store_kernel<T, size_t>, l.grid, b, 0, s, x, cols, xs, l.ld, l.total, codes, scales);
+    return l.small ? launch_pdl(ckpt_store_ragged_kernel<T, uint32_t>, l.grid, b, 0, s, x, cols, xs, l.ld, (uint32_t)l.total, codes, scales)
+                   : launch_pdl(ckpt_store_ragged_kernel<T, size_t>, l.grid, b, 0, s, x, cols, xs, l.ld, l.total, codes, scales);
+}
+
+template <typename T>
+cudaError_t load(const int8_t* codes, const uint8_t* scales, int rows, int cols, T* x, long long xs, int num_sms, cudaStream_t s) {
+    const Launch l = plan(x, rows, cols, xs, num_sms);
+    const dim3 b(CK_THREADS);
+    if (l.vec)
+        return l.small ? launch_pdl(ckpt_load_kernel<T, uint32_t>, l.grid, b, 0, s, codes, scales, cols, l.ld, (uint32_t)l.total, x, xs)
+                       : launch_pdl(ckpt_load_kernel<T, size_t>, l.grid, b, 0, s, codes, scales, cols, l.ld, l.total, x, xs);
+    return l.small ? launch_pdl(ckpt_load_ragged_kernel<T, uint32_t>, l.grid, b, 0, s, codes, scales, cols, l.ld, (uint32_t)l.total, x, xs)
+                   : launch_pdl(ckpt_load_ragged_kernel<T, size_t>, l.grid, b, 0, s, codes, scales, cols, l.ld, l.total, x, xs);
+}
 
 }  // namespace
 
 cudaError_t launch_checkpoint_store(const void* x, int x_bf16, int rows, int cols, long long xs, int8_t* codes,
                                     uint8_t* scales, int num_sms, cudaStream_t s) {
-    const int ld = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
-    const size_t total = (size_t)rows * (ld / CK_VALS);
-    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0, grid = ckpt_grid(total, num_sms);
-    const auto* h = static_cast<const __nv_bfloat16*>(x);
-    const auto* f = static_cast<const float*>(x);
-    if (small_index(total, grid))
-        return x_bf16 ? store<__nv_bfloat16, uint32_t>(h, cols, xs, ld, total, vec, codes, scales, grid, s)
-                      : store<float, uint32_t>(f, cols, xs, ld, total, vec, codes, scales, grid, s);
-    return x_bf16 ? store<__nv_bfloat16, size_t>(h, cols, xs, ld, total, vec, codes, scales, grid, s)
-                  : store<float, size_t>(f, cols, xs, ld, total, vec, codes, scales, grid, s);
+    return x_bf16 ? store(static_cast<const __nv_bfloat16*>(x), rows, cols, xs, codes, scales, num_sms, s)
+                  : store(static_cast<const float*>(x), rows, cols, xs, codes, scales, num_sms, s);
 }
 
 cudaError_t launch_checkpoint_load(const int8_t* codes, const uint8_t* scales, int rows, int cols, void* x, int x_bf16,
                                    long long xs, int num_sms, cudaStream_t s) {
-    const int ld = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
-    const size_t total = (size_t)rows * (ld / CK_VALS);
-    const int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && xs % (x_bf16 ? 8 : 4) == 0, grid = ckpt_grid(total, num_sms);
-    auto* h = static_cast<__nv_bfloat16*>(x);
-    auto* f = static_cast<float*>(x);
-    if (small_index(total, grid))
-        return x_bf16 ? load<__nv_bfloat16, uint32_t>(codes, scales, cols, ld, total, h, xs, vec, grid, s)
-                      : load<float, uint32_t>(codes, scales, cols, ld, total, f, xs, vec, grid, s);
-    return x_bf16 ? load<__nv_bfloat16, size_t>(codes, scales, cols, ld, total, h, xs, vec, grid, s)
-                  : load<float, size_t>(codes, scales, cols, ld, total, f, xs, vec, grid, s);
+    return x_bf16 ? load(codes, scales, rows, cols, static_cast<__nv_bfloat16*>(x), xs, num_sms, s)
+                  : load(codes, scales, rows, cols, static_cast<float*>(x), xs, num_sms, s);
 }
 
 }  // namespace muon

@@ -657,44 +657,50 @@ __device__ __forceinline__ float grouped_clip_factor(const float* __restrict__ m
     return root > 0.f ? g_own / root : 0.f;     // an infinite logit gives g = 0
 }
 
-// One warp per row: the factor is found once, and rows that keep their values are not
-// touched.  Bound by memory (8 bytes an element of the clipped rows).
+// A block takes CLIP_RUN consecutive elements of one head, whose rows lie one after the other;
+// it finds the head's factor once, and heads that keep their values are not touched.  Bound
+// by memory (8 bytes an element of the clipped heads): 16-byte accesses from the first aligned
+// address of the run on, four of them in flight a thread.
+constexpr int CLIP_RUN = EW_THREADS * 16;
+
 __global__ void __launch_bounds__(EW_THREADS) qk_clip_grouped_kernel(float* __restrict__ wq, float* __restrict__ wk,
                                                                     const float* __restrict__ max_logits, int n_heads,
-                                                                    int n_kv_heads, int head_dim, int cols, float tau,
-                                                                    int vec) {
+                                                                    int n_kv_heads, size_t head_size, float tau) {
     pdl_trigger();
     pdl_wait();
-    const int q_rows = n_heads * head_dim, rows = q_rows + n_kv_heads * head_dim, group = n_heads / n_kv_heads;
-    const int lane = threadIdx.x & 31, warps = gridDim.x * (EW_THREADS / 32);
-    for (int r = blockIdx.x * (EW_THREADS / 32) + threadIdx.x / 32; r < rows; r += warps) {
-        const bool key = r >= q_rows;
-        const int row = key ? r - q_rows : r;
-        const float f = grouped_clip_factor(max_logits, row / head_dim, group, key, tau);
-        if (f == 1.0f) continue;
-        float* w = (key ? wk : wq) + (size_t)row * cols;
-        if (vec) {
-            for (int c = lane * 4; c < cols; c += 128) {
-                float4 x = *reinterpret_cast<float4*>(w + c);
-                x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-                *reinterpret_cast<float4*>(w + c) = x;
-            }
-        } else {
-            for (int c = lane; c < cols; c += 32) w[c] *= f;
-        }
+    const bool key = (int)blockIdx.y >= n_heads;
+    const int head = key ? (int)blockIdx.y - n_heads : (int)blockIdx.y;
+    const float f = grouped_clip_factor(max_logits, head, n_heads / n_kv_heads, key, tau);
+    if (f == 1.0f) return;
+    const size_t begin = (size_t)blockIdx.x * CLIP_RUN;
+    float* w = (key ? wk : wq) + (size_t)head * head_size + begin;
+    const int n = (int)min((size_t)CLIP_RUN, head_size - begin);
+    // elements before the first 16-byte boundary, then groups of four, then what is left
+    const int lead = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(w) & 15)) / 4) & 3), groups = (n - lead) / 4;
+    float4* w4 = reinterpret_cast<float4*>(w + lead);
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int g = (int)threadIdx.x + i * EW_THREADS;
+        if (g < groups) x[i] = w4[g];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int g = (int)threadIdx.x + i * EW_THREADS;
+        if (g < groups) w4[g] = make_float4(x[i].x * f, x[i].y * f, x[i].z * f, x[i].w * f);
+    }
+    const int e = (int)threadIdx.x < lead ? (int)threadIdx.x : 4 * groups + (int)threadIdx.x;
+    if (e < n && (e < lead || e >= lead + 4 * groups)) w[e] *= f;
 }
 
 }  // namespace
 
 cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
-                                   int head_dim, int cols, float tau, int num_sms, cudaStream_t s) {
-    const int vec = (cols % 4 == 0) && (reinterpret_cast<uintptr_t>(wq) % 16 == 0) &&
-                    (reinterpret_cast<uintptr_t>(wk) % 16 == 0);
-    const int rows = (n_heads + n_kv_heads) * head_dim;
-    const int blocks = std::min((rows + EW_THREADS / 32 - 1) / (EW_THREADS / 32), num_sms * 8);
-    return launch_pdl(qk_clip_grouped_kernel, dim3(blocks), dim3(EW_THREADS), 0, s, wq, wk, max_logits, n_heads,
-                      n_kv_heads, head_dim, cols, tau, vec);
+                                   int head_dim, int cols, float tau, cudaStream_t s) {
+    const size_t head_size = (size_t)head_dim * cols;
+    const dim3 grid((unsigned)((head_size + CLIP_RUN - 1) / CLIP_RUN), (unsigned)(n_heads + n_kv_heads));
+    return launch_pdl(qk_clip_grouped_kernel, grid, dim3(EW_THREADS), 0, s, wq, wk, max_logits, n_heads, n_kv_heads, head_size,
+                      tau);
 }
 
 cudaError_t launch_qk_clip(float* wq, float* wk, const float* max_logits, int n_heads, int head_dim, int cols,

@@ -83,6 +83,6 @@ struct WgradMaps {
 cudaError_t launch_weight_grad(const WgradParams& p, const WgradMaps& maps, cudaStream_t s);
 
 cudaError_t launch_qk_clip_grouped(float* wq, float* wk, const float* max_logits, int n_heads, int n_kv_heads,
-                                   int head_dim, int cols, float tau, int num_sms, cudaStream_t s);
+                                   int head_dim, int cols, float tau, cudaStream_t s);
 
 }  // namespace muon

@@ -26,13 +26,13 @@ constexpr int WG_BK = 64;                       // tokens a stage
 constexpr int WG_OPERAND = 128 * WG_BK * 2;     // bytes of this CTA's half of an operand
 constexpr int WG_CHUNK = 64 * WG_BK * 2;        // 64 columns of it: 128-byte lines, one per token
 constexpr int WG_CODES = 128 * WG_BK;           // bytes of the codes of this CTA's 128 columns
-constexpr int WG_STAGES = 5;
+constexpr int WG_STAGES = 4;                    // (5 are no faster)
 constexpr int WG_CLUSTERS = 74;                 // CTA pairs of a B200
-constexpr int WG_EPI_WARPS = 4, WG_CVT_WARPS = 8;
+constexpr int WG_EPI_WARPS = 8, WG_CVT_WARPS = 8;    // (epilogue: two warps for 32 rows, half of the columns each)
 constexpr int WG_THREADS = 32 * (WG_EPI_WARPS + WG_CVT_WARPS + 2);
 constexpr int WG_TMA_WARP = WG_EPI_WARPS + WG_CVT_WARPS, WG_MMA_WARP = WG_TMA_WARP + 1;
 constexpr int WG_GROUP = 8;                     // stages whose scales a thread fetches at once
-constexpr int WG_SMEM = 1024 + WG_STAGES * (2 * WG_OPERAND + WG_CODES) + 8 * (3 * WG_STAGES + 5) + 32;
+constexpr int WG_SMEM = 1024 + WG_STAGES * (2 * WG_OPERAND + WG_CODES) + 8 * (3 * WG_STAGES + 5) + 32 + WG_EPI_WARPS * 32 * 33 * 4;
 constexpr int WG_MIN_BLOCKS = 4;                // fewest 64-token blocks of a split
 
 constexpr int ERR_WG_LOAD = 0x221, ERR_WG_CVT = 0x222, ERR_WG_MMA = 0x223, ERR_WG_EPI = 0x224;
@@ -102,50 +102,28 @@ __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 
-// 32 finished values of one row of G.
-__device__ __forceinline__ void store_run(const WgradParams& p, int row, int col, const uint32_t (&v)[32]) {
-    const size_t at = (size_t)row * p.cols + col;
-    if (p.g_bf16) {
-        __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.g) + at;
-        if (p.vec && col + 32 <= p.cols) {
+// A warp's 32 x 32 block of G, a row a lane, goes through its buffer so that every store of the
+// warp is 32 neighbours of one row: 32 lines a store otherwise, and G's rows may start at any
+// address.
+constexpr int WG_BUF = 32 * 33 * 4;
+
+template <typename T>
+__device__ __forceinline__ void store_block(const WgradParams& p, int row0, int col, const uint32_t (&v)[32], float* buf) {
+    const int lane = (int)(threadIdx.x & 31u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-                uint4 old = make_uint4(0, 0, 0, 0);
-                if (p.accumulate) old = reinterpret_cast<const uint4*>(g)[i];
-                const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+    for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = __uint_as_float(v[i]);
+    __syncwarp();
+    T* g = static_cast<T*>(p.g) + (size_t)row0 * p.cols + col + lane;
+    const int rows = min(32, p.rows - row0);
+    if (col + lane < p.cols) {
+        float old[32];          // all rows of G in flight at once
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(
-                        __uint_as_float(v[8 * i + 2 * e]) + __uint_as_float(o[e] << 16),
-                        __uint_as_float(v[8 * i + 2 * e + 1]) + __uint_as_float(o[e] & 0xFFFF0000u));
-                    w[e] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                reinterpret_cast<uint4*>(g)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
+        for (int r = 0; r < 32; ++r) old[r] = p.accumulate && r < rows ? (float)g[(size_t)r * p.cols] : 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col + i < p.cols)
-                    g[i] = __float2bfloat16_rn(__uint_as_float(v[i]) + (p.accumulate ? __bfloat162float(g[i]) : 0.f));
-        }
-    } else {
-        float* g = static_cast<float*>(p.g) + at;
-        if (p.vec && col + 32 <= p.cols) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (p.accumulate) old = reinterpret_cast<const float4*>(g)[i];
-                reinterpret_cast<float4*>(g)[i] =
-                    make_float4(__uint_as_float(v[4 * i]) + old.x, __uint_as_float(v[4 * i + 1]) + old.y,
-                                __uint_as_float(v[4 * i + 2]) + old.z, __uint_as_float(v[4 * i + 3]) + old.w);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col + i < p.cols) g[i] = __uint_as_float(v[i]) + (p.accumulate ? g[i] : 0.f);
-        }
+        for (int r = 0; r < 32; ++r)
+            if (r < rows) g[(size_t)r * p.cols] = (T)(buf[r * 33 + lane] + old[r]);
     }
+    __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WG_THREADS, 1)
@@ -286,6 +264,7 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
         }
     } else {
         const int lane = (int)(threadIdx.x & 31u);
+        float* buf = reinterpret_cast<float*>(tmem_slot + 2) + warp * (WG_BUF / 4);
         bool ok = true;
         WgUnit u;
         for (int i = 0; ok && unit_of(p, cid, i, u); ++i) {
@@ -293,15 +272,15 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
             ok = mbar_wait(&tfull[acc], (uint32_t)(i >> 1) & 1u, abort_flag, p.err, ERR_WG_EPI);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            const int in_tile = (int)rank * 128 + (int)warp * 32 + lane;
-            const int row = u.tile / p.tiles_n * WG_TILE + in_tile, col0 = u.tile % p.tiles_n * WG_TILE;
-            const uint32_t t_acc = tmem + acc * 256u + (warp * 32u << 16);
+            const int in_tile = (int)rank * 128 + (int)(warp & 3u) * 32, c0 = (int)(warp >> 2) * 4;
+            const int row0 = u.tile / p.tiles_n * WG_TILE + in_tile, col0 = u.tile % p.tiles_n * WG_TILE;
+            const uint32_t t_acc = tmem + acc * 256u + ((warp & 3u) * 32u << 16);
             // partial sums lie as 32 x 32 blocks, each as eight groups of four columns: a store of the warp
             // covers 512 bytes (a row per lane: 32 lines a store)
             float4* part = u.slot >= 0 ? reinterpret_cast<float4*>(p.partial) +
                                              ((size_t)u.slot * 8 + in_tile / 32) * (WG_TILE * 8) + lane : nullptr;
 #pragma unroll 1
-            for (int c = 0; c < WG_TILE / 32 && col0 + 32 * c < p.cols; ++c) {
+            for (int c = c0; c < c0 + 4 && col0 + 32 * c < p.cols; ++c) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(t_acc + 32u * c, v);
                 tmem_ld_wait();
@@ -310,8 +289,12 @@ weight_grad_kernel(const __grid_constant__ WgradParams p, const __grid_constant_
                     for (int e = 0; e < 8; ++e)
                         part[c * 256 + e * 32] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                                              __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                } else if (row < p.rows) {
-                    store_run(p, row, col0 + 32 * c, v);
+                } else if (row0 >= p.rows) {
+                    break;
+                } else if (p.g_bf16) {
+                    store_block<__nv_bfloat16>(p, row0, col0 + 32 * c, v, buf);
+                } else {
+                    store_block<float>(p, row0, col0 + 32 * c, v, buf);
                 }
             }
             tc_fence_before();
