@@ -283,8 +283,8 @@ typedef struct {
  * updated in place (start an optimizer step's micro-batches from -inf; a NaN logit is
  * passed over with its row).  out, lse and max_logits may not overlap any buffer of the call
  * (strided views that interleave without sharing an element do not overlap).
- * Non-finite values in a sequence's own rows reach its outputs; the values of one
- * sequence, and of rows in none, never reach another's.
+ * Non-finite values reach the outputs of the queries that see them and no others: not
+ * those of earlier queries, nor of another sequence.
  * cu_seqlens values outside the rule above are seen by the kernels only: such a
  * sequence is passed over, and muon_sync reports MUON_ERR_INVALID. */
 typedef struct {
@@ -315,6 +315,8 @@ muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void
  * grad_out: layout of out; dq, dk, dv: layouts of q, k, v, written (rows of no
  * sequence are not; keys that no query sees get zero).  delta: scratch for
  * n_heads * total_q floats, written.  P and dS enter their products rounded to bf16.
+ * A query with a non-finite value of its own, or that sees one, makes its dq NaN, and dk
+ * and dv of the keys that it sees; no other gradient of the call.
  * dq, dk, dv and delta may not overlap any buffer of the call. */
 typedef struct {
     muon_attention_args forward;

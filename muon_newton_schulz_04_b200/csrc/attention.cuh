@@ -179,10 +179,63 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&v)[2][32]) {
 // index.  The caller orders the writes before the products that read the tile.
 template <int DP>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int rows, int t, int threads) {
+#pragma unroll 1
     for (int i = first * 8 + t; i < rows * 8; i += threads)
 #pragma unroll
         for (int c = 0; c < DP / 64; ++c)
             sts128(tile + (uint32_t)(c * rows) * 128u + (uint32_t)i * 16u, make_uint4(0, 0, 0, 0));
+}
+
+__device__ __forceinline__ __nv_bfloat162 bits_bf162(uint32_t w) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t saddr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(saddr));
+    return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t saddr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+// Sets infinities and NaN in rows [first, rows) of such a tile (0 <= first; none when rows <=
+// first) to zero; true when this thread
+// met one.  It looks for one first: a sum of the values times zero is NaN then (four products
+// for eight values, and loads that wait for no store).
+template <int DP>
+__device__ __forceinline__ bool clean_rows(uint32_t tile, int first, int rows_in_tile, int rows, int t, int threads) {
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+    __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+    const uint32_t end = (uint32_t)max(0, rows) * 128u;
+#pragma unroll 1
+    for (int c = 0; c < DP / 64; ++c)
+#pragma unroll 2
+        for (uint32_t at = (uint32_t)(first * 8 + t) * 16u; at < end; at += (uint32_t)threads * 16u) {
+            const uint4 v = lds128(tile + (uint32_t)(c * rows_in_tile) * 128u + at);
+            sum[0] = __hfma2(bits_bf162(v.x), zero, sum[0]);
+            sum[1] = __hfma2(bits_bf162(v.y), zero, sum[1]);
+            sum[2] = __hfma2(bits_bf162(v.z), zero, sum[2]);
+            sum[3] = __hfma2(bits_bf162(v.w), zero, sum[3]);
+        }
+    const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+    const bool met = !(__low2float(all) == 0.f && __high2float(all) == 0.f);
+    if (met) {
+#pragma unroll 1
+        for (int i = 0; i < DP / 64; ++i)
+#pragma unroll 1
+            for (uint32_t at = (uint32_t)(first * 8 + t) * 16u; at < end; at += (uint32_t)threads * 16u)
+#pragma unroll 1
+                for (uint32_t e = 0; e < 16; e += 4) {
+                    const uint32_t word = tile + (uint32_t)(i * rows_in_tile) * 128u + at + e;
+                    uint32_t v = lds32(word);
+                    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+                    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+                    sts32(word, v);
+                }
+    }
+    return met;
 }
 
 // ---------------------------------------------------------------- arithmetic

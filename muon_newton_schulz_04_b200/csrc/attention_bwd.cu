@@ -33,7 +33,8 @@
 namespace muon {
 namespace {
 
-constexpr int ERR_BW_LOAD = 0x211, ERR_BW_MMA = 0x212, ERR_BW_MATH = 0x213;
+constexpr int ERR_DQ_LOAD = 0x211, ERR_DQ_MMA = 0x212, ERR_DQ_MATH = 0x213, ERR_DQ_CLEAN = 0x214;
+constexpr int ERR_DKV_LOAD = 0x231, ERR_DKV_MMA = 0x232, ERR_DKV_MATH = 0x233, ERR_DKV_CLEAN = 0x234;
 
 // What both kernels share.
 template <int DP>
@@ -41,7 +42,7 @@ struct BwLayout {
     static constexpr int HALVES = DP / 64;                      // of a step's columns
     static constexpr int STEP = DP;                             // rows of a streamed tile
     static constexpr int MATH = 128 * HALVES, THREADS = MATH + 128;     // + a warpgroup: TMA, MMA, tensor memory
-    static constexpr int W_TMA = MATH / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 2;
+    static constexpr int W_TMA = MATH / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 2;     // W_TMEM and the last warp clean tiles
     static constexpr int CTAS = 2 / HALVES;                     // of an SM
     static constexpr int REGS = HALVES == 1 ? 128 : 168;        // a thread: at launch, then of the math warps and the others
     static constexpr int REGS_MATH = HALVES == 1 ? 168 : 200, REGS_OTHER = HALVES == 1 ? 88 : 104;
@@ -73,7 +74,7 @@ template <int DP>
 struct DqLayout : BwLayout<DP> {
     using Base = BwLayout<DP>;
     static constexpr int KS = DP == 64 ? 4 : 3, VS = DP == 64 ? 3 : 2;      // ring slots: K is used twice
-    static constexpr int BARRIERS = 2 + 2 * KS + 2 * VS + 6;
+    static constexpr int BARRIERS = 2 + 2 * KS + 2 * VS + 9;
     static constexpr int SMEM = 1024 + 2 * Base::OWN + (KS + VS) * Base::MOVING + 8 * BARRIERS + 2 * 128 * 4 + 64;
     static constexpr uint32_t S_COL = 0, DP_COL = 2 * DP, DQ_COL = 3 * DP;  // S: two buffers
     static_assert(SMEM <= Base::MOST_SMEM, "shared memory above the SM's 228 KiB");
@@ -94,8 +95,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     uint64_t* do_full = q_full + 1;
     uint64_t *k_full = do_full + 1, *k_empty = k_full + L::KS, *v_full = k_empty + L::KS, *v_empty = v_full + L::VS;
     uint64_t *s_full = v_empty + L::VS, *dp_full = s_full + 2, *dp_read = dp_full + 1, *ds_ready = dp_read + 1,
-             *dq_full = ds_ready + 1;
-    float* exch = reinterpret_cast<float*>(dq_full + 1);            // [2][128]
+             *dq_full = ds_ready + 2, *near = dq_full + 1, *clean = near + 1;
+    float* exch = reinterpret_cast<float*>(clean + 1);            // [2][128]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(exch + 256);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
@@ -126,8 +127,11 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
         mbar_init(dp_read, L::MATH);
-        mbar_init(ds_ready, L::MATH);
+        mbar_init(&ds_ready[0], L::MATH);               // one per buffer: dS may run a tile ahead of its wait
+        mbar_init(&ds_ready[1], L::MATH);
         mbar_init(dq_full, 1);
+        mbar_init(near, 1);                             // the next edge tile may be cleaned
+        mbar_init(clean, 2);                            // its K is fit for dS K
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -141,74 +145,95 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         const int row0 = info[1].x * AT_ROWS, shift = lk - lq, kv_head = head / p.group;
         const int last = min(row0 + AT_ROWS, lq) - 1 + shift;       // last key that any row sees
         const int n = last < 0 ? 0 : last / L::STEP + 1;
+        const int edge0 = max(0, row0 + shift + 1) / L::STEP;      // key tiles from this one on: some row does not see all of them
 
-        if (warp == L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && n > 0) {
-                mbar_arrive_expect_tx(q_full, L::OWN);
-                load_tile<DP, 128, AT_BWD_BOX>(s_q, &maps.q, q_full, head, q0 + row0);
+        if (warp >= L::W_TMA) {
+            regs_less<L::REGS_OTHER>();     // one instruction for all warps of the group
+            if (warp == L::W_TMA) {
+                if (elect_one() && n > 0) {
+                    mbar_arrive_expect_tx(q_full, L::OWN);
+                    load_tile<DP, 128, AT_BWD_BOX>(s_q, &maps.q, q_full, head, q0 + row0);
+                    bool ok = true;
+                    for (int j = 0; j < n + L::KS; ++j) {       // the last turns only wait for the loads to be used
+                        const int ks = j % L::KS, vs = j % L::VS;
+                        if (!mbar_wait(&k_empty[ks], ((uint32_t)(j / L::KS) & 1u) ^ 1u, abort_flag, p.err, ERR_DQ_LOAD)) { ok = false; break; }
+                        if (j < n) {
+                            mbar_arrive_expect_tx(&k_full[ks], L::MOVING);
+                            load_tile<DP, L::STEP, AT_BWD_BOX>(s_k + ks * L::MOVING, &maps.k, &k_full[ks], kv_head, k0 + j * L::STEP);
+                        }
+                        if (j == 0) {
+                            mbar_arrive_expect_tx(do_full, L::OWN);
+                            load_tile<DP, 128, AT_BWD_BOX>(s_do, &maps.go, do_full, head, q0 + row0);
+                        }
+                        if (j < n + L::VS &&
+                            !mbar_wait(&v_empty[vs], ((uint32_t)(j / L::VS) & 1u) ^ 1u, abort_flag, p.err, ERR_DQ_LOAD)) { ok = false; break; }
+                        if (j < n) {
+                            mbar_arrive_expect_tx(&v_full[vs], L::MOVING);
+                            load_tile<DP, L::STEP, AT_BWD_BOX>(s_v + vs * L::MOVING, &maps.v, &v_full[vs], kv_head, k0 + j * L::STEP);
+                        }
+                    }
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+                }
+            } else if (warp == L::W_MMA) {
+                if (elect_one() && n > 0) {
+                    const uint32_t q_s = smem_u32(s_q), do_s = smem_u32(s_do), k_s = smem_u32(s_k), v_s = smem_u32(s_v);
+                    auto wait = [&](uint64_t* b, int use) {
+                        const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_DQ_MMA);
+                        tc_fence_after();
+                        return ok;
+                    };
+                    auto do_s_product = [&](int j) {
+                        mma_abt<DP, L::STEP>(tmem + L::S_COL + (uint32_t)(DP * (j & 1)), q_s, k_s + (uint32_t)(j % L::KS) * L::MOVING);
+                        tc_commit(&s_full[j & 1]);
+                    };
+                    auto do_dp_product = [&](int j) {
+                        mma_abt<DP, L::STEP>(tmem + L::DP_COL, do_s, v_s + (uint32_t)(j % L::VS) * L::MOVING);
+                        tc_commit(dp_full);
+                        tc_commit(&v_empty[j % L::VS]);
+                    };
+                    bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
+                    if (ok) do_s_product(0);
+                    ok = ok && wait(do_full, 0) && wait(&v_full[0], 0);
+                    if (ok) do_dp_product(0);
+                    if (edge0 == 0) mbar_arrive(near);
+                    for (int j = 0; j < n && ok; ++j) {
+                        if (j + 1 < n) {
+                            // its buffer held dS of tile j - 1, whose product runs before
+                            if (!(ok = wait(&k_full[(j + 1) % L::KS], (j + 1) / L::KS))) break;
+                            do_s_product(j + 1);
+                            if (!(ok = wait(dp_read, j) && wait(&v_full[(j + 1) % L::VS], (j + 1) / L::VS))) break;
+                            do_dp_product(j + 1);
+                        }
+                        if (!(ok = wait(&ds_ready[j & 1], j >> 1) && (j < edge0 || wait(clean, j - edge0)))) break;
+                        if (j + 1 >= edge0 && j + 1 < n) mbar_arrive(near);
+                        for (int h = 0; h < L::HALVES; ++h)
+                            mma_tb_half<DP>(tmem + L::DQ_COL, tmem + L::S_COL + (uint32_t)(DP * (j & 1) + 64 * h),
+                                            k_s + (uint32_t)(j % L::KS) * L::MOVING, h, j > 0 || h > 0);
+                        tc_commit(&k_empty[j % L::KS]);
+                    }
+                    if (ok) tc_commit(dq_full);
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+                }
+            } else if (warp >= L::W_TMEM && warp < L::W_TMEM + 2) {
+                // dS is 0 for keys that a row does not see, but 0 times K need not be: rows behind the sequence's keys
+                // become zero, as do infinities and NaN of keys that some row does not see (rows that see them have
+                // lse = NaN).  Done here, when S has read the tile, while dS is formed.
+                const int lane = (int)threadIdx.x - 32 * L::W_TMEM;
                 bool ok = true;
-                for (int j = 0; j < n + L::KS; ++j) {       // the last turns only wait for the loads to be used
-                    const int ks = j % L::KS, vs = j % L::VS;
-                    if (!mbar_wait(&k_empty[ks], ((uint32_t)(j / L::KS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
-                    if (j < n) {
-                        mbar_arrive_expect_tx(&k_full[ks], L::MOVING);
-                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_k + ks * L::MOVING, &maps.k, &k_full[ks], kv_head, k0 + j * L::STEP);
-                    }
-                    if (j == 0) {
-                        mbar_arrive_expect_tx(do_full, L::OWN);
-                        load_tile<DP, 128, AT_BWD_BOX>(s_do, &maps.go, do_full, head, q0 + row0);
-                    }
-                    if (j < n + L::VS &&
-                        !mbar_wait(&v_empty[vs], ((uint32_t)(j / L::VS) & 1u) ^ 1u, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
-                    if (j < n) {
-                        mbar_arrive_expect_tx(&v_full[vs], L::MOVING);
-                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_v + vs * L::MOVING, &maps.v, &v_full[vs], kv_head, k0 + j * L::STEP);
-                    }
+                for (int j = edge0; j < n && ok; ++j) {
+                    ok = mbar_wait(near, (uint32_t)(j - edge0) & 1u, abort_flag, p.err, ERR_DQ_CLEAN) &&
+                         mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_DQ_CLEAN);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t tile = smem_u32(s_k + (j % L::KS) * L::MOVING);
+                    const int behind = lk - j * L::STEP;
+                    if (behind < L::STEP) zero_rows<DP>(tile, behind, L::STEP, lane, 64);
+                    clean_rows<DP>(tile, max(0, row0 + shift + 1 - j * L::STEP), L::STEP, min(L::STEP, behind), lane, 64);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(clean);
                 }
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
-        } else if (warp == L::W_MMA) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && n > 0) {
-                const uint32_t q_s = smem_u32(s_q), do_s = smem_u32(s_do), k_s = smem_u32(s_k), v_s = smem_u32(s_v);
-                auto wait = [&](uint64_t* b, int use) {
-                    const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_BW_MMA);
-                    tc_fence_after();
-                    return ok;
-                };
-                auto do_s_product = [&](int j) {
-                    mma_abt<DP, L::STEP>(tmem + L::S_COL + (uint32_t)(DP * (j & 1)), q_s, k_s + (uint32_t)(j % L::KS) * L::MOVING);
-                    tc_commit(&s_full[j & 1]);
-                };
-                auto do_dp_product = [&](int j) {
-                    mma_abt<DP, L::STEP>(tmem + L::DP_COL, do_s, v_s + (uint32_t)(j % L::VS) * L::MOVING);
-                    tc_commit(dp_full);
-                    tc_commit(&v_empty[j % L::VS]);
-                };
-                bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
-                if (ok) do_s_product(0);
-                ok = ok && wait(do_full, 0) && wait(&v_full[0], 0);
-                if (ok) do_dp_product(0);
-                for (int j = 0; j < n && ok; ++j) {
-                    if (j + 1 < n) {
-                        // its buffer held dS of tile j - 1, whose product runs before
-                        if (!(ok = wait(&k_full[(j + 1) % L::KS], (j + 1) / L::KS))) break;
-                        do_s_product(j + 1);
-                        if (!(ok = wait(dp_read, j) && wait(&v_full[(j + 1) % L::VS], (j + 1) / L::VS))) break;
-                        do_dp_product(j + 1);
-                    }
-                    if (!(ok = wait(ds_ready, j))) break;
-                    for (int h = 0; h < L::HALVES; ++h)
-                        mma_tb_half<DP>(tmem + L::DQ_COL, tmem + L::S_COL + (uint32_t)(DP * (j & 1) + 64 * h),
-                                        k_s + (uint32_t)(j % L::KS) * L::MOVING, h, j > 0 || h > 0);
-                    tc_commit(&k_empty[j % L::KS]);
-                }
-                if (ok) tc_commit(dq_full);
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
-            }
-        } else if (warp >= L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
         } else {
             regs_more<L::REGS_MATH>();
             const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
@@ -254,7 +279,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             bool ok = true;
             for (int j = 0; j < n; ++j) {
                 // (with one step the warps meet in barriers: one whose wait gave up goes on without waiting)
-                ok = mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = mbar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag, p.err, ERR_DQ_MATH);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok && n > 1) break;
                 tc_fence_after();
@@ -276,7 +301,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     s[i / 32][i % 32] = __float_as_uint(x);
                     s[i / 32][i % 32 + 1] = __float_as_uint(y);
                 }
-                ok = ok && mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = ok && mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag, p.err, ERR_DQ_MATH);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok && n > 1) break;
                 tc_fence_after();
@@ -284,8 +309,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 load64(tmem + lane_base + L::DP_COL + 64u * half, dp);
                 tc_fence_before();
                 mbar_arrive(dp_read);
-                // column of the last seen key; a row that sees one key has P = 1 and dS = 0, exactly
-                const int seen = row + shift == 0 ? -1 : row + shift - j * L::STEP - 64 * half;
+                int seen = row + shift - j * L::STEP - 64 * half;           // column of the last seen key
                 const bool edge = (j + 1) * L::STEP > row0 + shift + 1;
                 if (n == 1) {
                     // few keys: O's rounding in D is not small beside dP, and D = sum_j P_ij dP_ij is at hand
@@ -306,6 +330,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         D += exch[(half ^ 1) * 128 + t];
                     }
                 }
+                if (row + shift == 0 && isfinite(D)) seen = -1;             // one key: P = 1 and dS = 0, exactly
                 const uint64_t d2 = pack2(-D, -D);
                 uint32_t ds[32];
                 uint64_t sum2 = pack2(0.f, 0.f);
@@ -327,17 +352,12 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 unpack2(sum2, a, b);
                 rest += a + b;
                 tmem_st_32x32b_x32(s_t, ds);
-                if (lk - j * L::STEP < L::STEP) {
-                    // rows behind the sequence's keys: dS is 0 there, but 0 times what lies behind need not be
-                    zero_rows<DP>(smem_u32(s_k + (j % L::KS) * L::MOVING), lk - j * L::STEP, L::STEP, (int)threadIdx.x, L::MATH);
-                    fence_proxy_async_smem();
-                }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(ds_ready);
+                mbar_arrive(&ds_ready[j & 1]);
             }
             if (ok && n > 0) {
-                ok = mbar_wait(dq_full, 0, abort_flag, p.err, ERR_BW_MATH);
+                ok = mbar_wait(dq_full, 0, abort_flag, p.err, ERR_DQ_MATH);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             }
@@ -372,7 +392,7 @@ template <int DP>
 struct DkvLayout : BwLayout<DP> {
     using Base = BwLayout<DP>;
     static constexpr int SLOTS = DP == 64 ? 3 : 2;              // of q and of dO
-    static constexpr int BARRIERS = 2 + 4 * SLOTS + 6;
+    static constexpr int BARRIERS = 2 + 4 * SLOTS + 9;
     static constexpr int ONES = 128 * 16 * 2, EXTRA = Base::STEP * 16 * 2;      // 16 more columns of the tiles
     static constexpr int SMEM = 1024 + ONES + 4 * EXTRA + 2 * Base::OWN + 2 * SLOTS * Base::MOVING + 8 * BARRIERS + 64;
     static constexpr uint32_t S_COL = 0, DP_COL = DP, DK_COL = 2 * DP, DV_COL = 3 * DP;
@@ -393,8 +413,8 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     uint64_t* extra_ready = kv_full + 1;        // the ones, and the first item's columns
     uint64_t *q_full = extra_ready + 1, *q_empty = q_full + L::SLOTS, *do_full = q_empty + L::SLOTS, *do_empty = do_full + L::SLOTS;
     uint64_t *s_full = do_empty + L::SLOTS, *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 2,
-             *dkv_full = ds_ready + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkv_full + 1);
+             *dkv_full = ds_ready + 1, *near = dkv_full + 1, *clean_do = near + 1, *clean_q = clean_do + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean_q + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
     int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
@@ -432,6 +452,9 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         mbar_init(&p_ready[1], L::MATH);
         mbar_init(ds_ready, L::MATH);
         mbar_init(dkv_full, 1);
+        mbar_init(near, 1);                     // the next edge item may be cleaned
+        mbar_init(clean_do, 2);                 // its dO is fit for P^T dO
+        mbar_init(clean_q, 2);                  // its Q is fit for dS^T Q
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -445,89 +468,129 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         const int key0 = info[1].x * AT_ROWS, shift = lk - lq;
         const int tiles = (lq + L::STEP - 1) / L::STEP, first = max(0, key0 - shift) / L::STEP;   // query tiles that see any of the keys
         const int per_head = max(0, tiles - first), n = per_head * p.group;
-        // item `it`: query tile first + it % per_head of head kv_head * group + it / per_head
+        // item `it`: query tile first + it % per_head of head kv_head * group + it / per_head; an edge item holds
+        // queries that do not see every key of the CTA, or rows behind the sequence's queries
+        const int diagonal = max(0, key0 + AT_ROWS - 1 - shift + L::STEP - 1) / L::STEP, partial = lq / L::STEP;
+        auto is_edge = [&](int tile) { return tile < diagonal || tile >= partial; };
 
-        if (warp == L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && n > 0) {
-                mbar_arrive_expect_tx(kv_full, 2 * L::OWN);
-                load_tile<DP, 128, AT_BWD_BOX>(s_k, &maps.k, kv_full, kv_head, k0 + key0);
-                load_tile<DP, 128, AT_BWD_BOX>(s_v, &maps.v, kv_full, kv_head, k0 + key0);
-                bool ok = true;
-                int tile = first, head = kv_head * p.group;
-                for (int it = 0; it < n + L::SLOTS; ++it) {     // the last turns only wait for the loads to be used
-                    const int slot = it % L::SLOTS;
-                    const uint32_t par = ((uint32_t)(it / L::SLOTS) & 1u) ^ 1u;
-                    if (!mbar_wait(&q_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
-                    if (it < n) {
-                        mbar_arrive_expect_tx(&q_full[slot], L::MOVING);
-                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_q + slot * L::MOVING, &maps.q, &q_full[slot], head, q0 + tile * L::STEP);
+        if (warp >= L::W_TMA) {
+            regs_less<L::REGS_OTHER>();     // one instruction for all warps of the group
+            if (warp == L::W_TMA) {
+                if (elect_one() && n > 0) {
+                    mbar_arrive_expect_tx(kv_full, 2 * L::OWN);
+                    load_tile<DP, 128, AT_BWD_BOX>(s_k, &maps.k, kv_full, kv_head, k0 + key0);
+                    load_tile<DP, 128, AT_BWD_BOX>(s_v, &maps.v, kv_full, kv_head, k0 + key0);
+                    bool ok = true;
+                    int tile = first, head = kv_head * p.group;
+                    for (int it = 0; it < n + L::SLOTS; ++it) {     // the last turns only wait for the loads to be used
+                        const int slot = it % L::SLOTS;
+                        const uint32_t par = ((uint32_t)(it / L::SLOTS) & 1u) ^ 1u;
+                        if (!mbar_wait(&q_empty[slot], par, abort_flag, p.err, ERR_DKV_LOAD)) { ok = false; break; }
+                        if (it < n) {
+                            mbar_arrive_expect_tx(&q_full[slot], L::MOVING);
+                            load_tile<DP, L::STEP, AT_BWD_BOX>(s_q + slot * L::MOVING, &maps.q, &q_full[slot], head, q0 + tile * L::STEP);
+                        }
+                        if (!mbar_wait(&do_empty[slot], par, abort_flag, p.err, ERR_DKV_LOAD)) { ok = false; break; }
+                        if (it < n) {
+                            mbar_arrive_expect_tx(&do_full[slot], L::MOVING);
+                            load_tile<DP, L::STEP, AT_BWD_BOX>(s_do + slot * L::MOVING, &maps.go, &do_full[slot], head, q0 + tile * L::STEP);
+                        }
+                        if (++tile == tiles) { tile = first; ++head; }
                     }
-                    if (!mbar_wait(&do_empty[slot], par, abort_flag, p.err, ERR_BW_LOAD)) { ok = false; break; }
-                    if (it < n) {
-                        mbar_arrive_expect_tx(&do_full[slot], L::MOVING);
-                        load_tile<DP, L::STEP, AT_BWD_BOX>(s_do + slot * L::MOVING, &maps.go, &do_full[slot], head, q0 + tile * L::STEP);
-                    }
-                    if (++tile == tiles) { tile = first; ++head; }
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
                 }
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
-            }
-        } else if (warp == L::W_MMA) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && n > 0) {
-                const uint32_t k_s = smem_u32(s_k), v_s = smem_u32(s_v), q_s = smem_u32(s_q), do_s = smem_u32(s_do);
-                auto wait = [&](uint64_t* b, int use) {
-                    const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_BW_MMA);
-                    tc_fence_after();
-                    return ok;
-                };
-                // S^T - lse / scale and dP^T - D
-                const uint32_t ones_s = smem_u32(s_ones), lse_s = smem_u32(s_lse), d_s = smem_u32(s_d);
-                auto do_s_product = [&](int it, uint32_t q) {
-                    mma_abt<DP, L::STEP>(tmem + L::S_COL, k_s, q);
-                    mma_extra<L::STEP>(tmem + L::S_COL, ones_s, lse_s + (uint32_t)(it & 1) * L::EXTRA);
-                    tc_commit(s_full);
-                };
-                auto do_dp_product = [&](int it, uint32_t dout) {
-                    mma_abt<DP, L::STEP>(tmem + L::DP_COL, v_s, dout);
-                    mma_extra<L::STEP>(tmem + L::DP_COL, ones_s, d_s + (uint32_t)(it & 1) * L::EXTRA);
-                    tc_commit(dp_full);
-                };
-                auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
-                auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
-                bool ok = wait(kv_full, 0) && wait(&q_full[0], 0) && wait(extra_ready, 0);
-                if (ok) do_s_product(0, q_at(0));
-                ok = ok && wait(&do_full[0], 0);
-                if (ok) do_dp_product(0, do_at(0));
-                for (int it = 0; it < n && ok; ++it) {
-                    const bool more = it + 1 < n;
-                    for (int c = 0; c < 2 && ok; ++c) {
-                        if (!(ok = wait(&p_ready[c], it))) break;
+            } else if (warp == L::W_MMA) {
+                if (elect_one() && n > 0) {
+                    const uint32_t k_s = smem_u32(s_k), v_s = smem_u32(s_v), q_s = smem_u32(s_q), do_s = smem_u32(s_do);
+                    auto wait = [&](uint64_t* b, int use) {
+                        const bool ok = mbar_wait(b, (uint32_t)use & 1u, abort_flag, p.err, ERR_DKV_MMA);
+                        tc_fence_after();
+                        return ok;
+                    };
+                    // S^T - lse / scale and dP^T - D
+                    const uint32_t ones_s = smem_u32(s_ones), lse_s = smem_u32(s_lse), d_s = smem_u32(s_d);
+                    auto do_s_product = [&](int it, uint32_t q) {
+                        mma_abt<DP, L::STEP>(tmem + L::S_COL, k_s, q);
+                        mma_extra<L::STEP>(tmem + L::S_COL, ones_s, lse_s + (uint32_t)(it & 1) * L::EXTRA);
+                        tc_commit(s_full);
+                    };
+                    auto do_dp_product = [&](int it, uint32_t dout) {
+                        mma_abt<DP, L::STEP>(tmem + L::DP_COL, v_s, dout);
+                        mma_extra<L::STEP>(tmem + L::DP_COL, ones_s, d_s + (uint32_t)(it & 1) * L::EXTRA);
+                        tc_commit(dp_full);
+                    };
+                    auto q_at = [&](int it) { return q_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
+                    auto do_at = [&](int it) { return do_s + (uint32_t)(it % L::SLOTS) * L::MOVING; };
+                    bool ok = wait(kv_full, 0) && wait(&q_full[0], 0) && wait(extra_ready, 0);
+                    if (ok) do_s_product(0, q_at(0));
+                    ok = ok && wait(&do_full[0], 0);
+                    if (ok) do_dp_product(0, do_at(0));
+                    int tile = first, edges = 0;
+                    for (int it = 0; it < n && ok; ++it) {
+                        const bool more = it + 1 < n, edge = is_edge(tile);
+                        if (++tile == tiles) tile = first;
+                        if (it == 0 && edge) mbar_arrive(near);
+                        for (int c = 0; c < 2 && ok; ++c) {
+                            if (!(ok = wait(&p_ready[c], it))) break;
+                            if (c == 0 && edge && !(ok = wait(clean_do, edges))) break;
+                            for (int h = 0; h < L::HALVES; ++h)
+                                mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 64u * h + 16u * c, do_at(it), 2 * h + c,
+                                                   it > 0 || c > 0 || h > 0);
+                        }
+                        if (!ok) break;
+                        tc_commit(&do_empty[it % L::SLOTS]);
+                        if (more && is_edge(tile)) mbar_arrive(near);
+                        // (here already: the next item's Q may be cleaned as soon as its S^T is there)
+                        if (edge && !(ok = wait(clean_q, edges++))) break;
+                        if (more) {
+                            // the next S^T takes the place of P^T: products run in order
+                            if (!(ok = wait(&q_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
+                            do_s_product(it + 1, q_at(it + 1));
+                        }
+                        if (!(ok = wait(ds_ready, it))) break;
                         for (int h = 0; h < L::HALVES; ++h)
-                            mma_tb_quarter<DP>(tmem + L::DV_COL, tmem + L::S_COL + 64u * h + 16u * c, do_at(it), 2 * h + c,
-                                               it > 0 || c > 0 || h > 0);
+                            mma_tb_half<DP>(tmem + L::DK_COL, tmem + L::DP_COL + 64u * h, q_at(it), h, it > 0 || h > 0);
+                        tc_commit(&q_empty[it % L::SLOTS]);
+                        if (more) {
+                            if (!(ok = wait(&do_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
+                            do_dp_product(it + 1, do_at(it + 1));
+                        }
                     }
-                    if (!ok) break;
-                    tc_commit(&do_empty[it % L::SLOTS]);
-                    if (more) {
-                        // the next S^T takes the place of P^T: products run in order
-                        if (!(ok = wait(&q_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
-                        do_s_product(it + 1, q_at(it + 1));
-                    }
-                    if (!(ok = wait(ds_ready, it))) break;
-                    for (int h = 0; h < L::HALVES; ++h)
-                        mma_tb_half<DP>(tmem + L::DK_COL, tmem + L::DP_COL + 64u * h, q_at(it), h, it > 0 || h > 0);
-                    tc_commit(&q_empty[it % L::SLOTS]);
-                    if (more) {
-                        if (!(ok = wait(&do_full[(it + 1) % L::SLOTS], (it + 1) / L::SLOTS))) break;
-                        do_dp_product(it + 1, do_at(it + 1));
+                    if (ok) tc_commit(dkv_full);
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+                }
+            } else if (warp >= L::W_TMEM && warp < L::W_TMEM + 2) {
+                // P and dS are 0 for queries that do not see a key, but 0 times dO or Q need not be: rows behind the
+                // sequence's queries become zero, as do infinities and NaN of queries that do not see every key (keys
+                // that they see get NaN all the same: by lse, or by D, which is not finite then).  Done here while S and
+                // P are formed: dO when it has arrived (what dP^T makes of the rows that change does not matter, as P
+                // is NaN or 0 there), Q when S^T has read it.
+                const int lane = (int)threadIdx.x - 32 * L::W_TMEM;
+                bool ok = true;
+                int tile = first, edges = 0;
+                for (int it = 0; it < n && ok; ++it) {
+                    const int row0 = tile * L::STEP, slot = it % L::SLOTS;
+                    const bool edge = is_edge(tile);
+                    if (++tile == tiles) tile = first;
+                    if (!edge) continue;
+                    const int behind = lq - row0, blind = min(min(L::STEP, behind), key0 + AT_ROWS - 1 - shift - row0);
+                    // (one loop and one copy of its code: few CTAs find it in the instruction cache)
+#pragma unroll 1
+                    for (int i = 0; i < 3 && ok; ++i) {
+                        uint64_t* bar = i == 0 ? near : i == 1 ? &do_full[slot] : s_full;
+                        const uint32_t use = (uint32_t)(i == 0 ? edges++ : i == 1 ? it / L::SLOTS : it);
+                        ok = mbar_wait(bar, use & 1u, abort_flag, p.err, ERR_DKV_CLEAN);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok || i == 0) continue;
+                        const uint32_t tile_s = smem_u32((i == 1 ? s_do : s_q) + slot * L::MOVING);
+                        zero_rows<DP>(tile_s, behind, L::STEP, lane, 64);
+                        clean_rows<DP>(tile_s, 0, L::STEP, blind, lane, 64);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (elect_one()) mbar_arrive(i == 1 ? clean_do : clean_q);
                     }
                 }
-                if (ok) tc_commit(dkv_full);
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
             }
-        } else if (warp >= L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
         } else {
             regs_more<L::REGS_MATH>();
             const int t = (int)(threadIdx.x & 127u), half = (int)(warp >> 2);
@@ -557,17 +620,20 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 const float hi = __bfloat162float(__float2bfloat16_rn(v));
                 const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
                 const uint32_t at = extra_s + (uint32_t)(item & 1) * L::EXTRA;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(at), "r"(bf16x2(hi, mid)),
-                             "r"(bf16x2(v - hi - mid, 0.f)) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" :: "r"(at), "r"(bf16x2(hi, mid)) : "memory");
+                asm volatile("st.shared.b16 [%0], %1;" :: "r"(at + 4u), "h"((uint16_t)bf16x2(v - hi - mid, 0.f)) : "memory");
+                // 0 * D in the fourth column beside Q: a row whose D is not finite gets P = NaN where it sees a key
+                if (brings_d)
+                    asm volatile("st.shared.b16 [%0], %1;" :: "r"(at - 2u * L::EXTRA + 6u), "h"((uint16_t)bf16x2(0.f * v, 0.f)) : "memory");
             };
             float next = 0.f;
             pdl_wait();                             // D is there
             if (n > 0) {
-                // columns 0-2 of the ones are 1, all others of the extra columns 0
+                // columns 0-3 of the ones are 1, what is not written below of the extra columns 0
                 const uint4 zero = make_uint4(0, 0, 0, 0);
                 for (int i = (int)threadIdx.x; i < (L::ONES + 4 * L::EXTRA) / 16; i += L::MATH) sts128(smem_u32(smem) + 16u * i, zero);
                 math_sync<DP>();
-                if (half == 0) sts128(smem_u32(s_ones) + extra_at(t), make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u));
+                if (half == 0) sts128(smem_u32(s_ones) + extra_at(t), make_uint4(0x3F803F80u, 0x3F803F80u, 0u, 0u));
                 put(0, fetch(0));
                 next = fetch(1);
                 fence_proxy_async_smem();
@@ -580,24 +646,16 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     next = fetch(it + 2);
                 }
                 const int row0 = tile * L::STEP;
+                const bool edge = is_edge(tile);
                 if (++tile == tiles) { tile = first; ++head; }
                 // query i of the tile sees this thread's key when i >= unseen; rows from lq on are none
                 const int unseen = key - shift - row0 - 64 * half, live = lq - row0 - 64 * half;
-                const bool edge = key0 + AT_ROWS - 1 > row0 + shift || row0 + L::STEP > lq;
 
-                ok = mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = mbar_wait(s_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_DKV_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32];
                 load64(s_t, s);
-                if (row0 + L::STEP > lq) {
-                    // rows behind the sequence's queries: P and dS are 0 there, but 0 times what lies behind need not be
-                    ok = mbar_wait(&do_full[it % L::SLOTS], (uint32_t)(it / L::SLOTS) & 1u, abort_flag, p.err, ERR_BW_MATH);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    zero_rows<DP>(smem_u32(s_do + (it % L::SLOTS) * L::MOVING), lq - row0, L::STEP, (int)threadIdx.x, L::MATH);
-                    zero_rows<DP>(smem_u32(s_q + (it % L::SLOTS) * L::MOVING), lq - row0, L::STEP, (int)threadIdx.x, L::MATH);
-                    fence_proxy_async_smem();
-                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -628,7 +686,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     mbar_arrive(&p_ready[q]);
                 }
 
-                ok = mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_BW_MATH);
+                ok = mbar_wait(dp_full, (uint32_t)it & 1u, abort_flag, p.err, ERR_DKV_MATH);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t dp[2][32], pr[32];
@@ -654,7 +712,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 mbar_arrive(ds_ready);
             }
             if (ok && n > 0) {
-                ok = mbar_wait(dkv_full, 0, abort_flag, p.err, ERR_BW_MATH);
+                ok = mbar_wait(dkv_full, 0, abort_flag, p.err, ERR_DKV_MATH);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             }

@@ -35,13 +35,15 @@ struct FwLayout {
     static constexpr int THREADS = SOFTMAX + 128;                   // + a warpgroup: TMA, an MMA warp per tile, tensor memory
     static constexpr int CTAS = 2 / TILES;                          // of an SM
     static constexpr int W_TMA = SOFTMAX / 32, W_MMA = W_TMA + 1, W_TMEM = W_TMA + 3;
+    static constexpr int W_CLEAN = W_MMA + TILES, CLEANERS = 3 - TILES;     // W_TMEM and, with one tile, the warp before it
     // registers a thread: at launch, then of the softmax warpgroups and the other one
     static constexpr int REGS = TILES == 1 ? 128 : 168;
     static constexpr int REGS_SOFTMAX = TILES == 1 ? 200 : 216, REGS_OTHER = TILES == 1 ? 56 : 72;
     static_assert(SOFTMAX * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS, "more registers than launched with");
     static constexpr int TILE = DP / 64 * AT_CHUNK;                 // bytes of a q, k or v tile
     static constexpr int SLOTS = 5;                                 // ring of k and v tiles
-    static constexpr int BARRIERS = 1 + 2 * SLOTS + 6 * TILES;
+    static constexpr int EDGES = TILES + 1;                         // most key tiles that not every row sees all of
+    static constexpr int BARRIERS = 1 + 2 * SLOTS + 6 * TILES + 1 + EDGES;
     static constexpr int SMEM = (TILES + SLOTS) * TILE + 8 * BARRIERS + 64;
     static constexpr bool P_APART = DP == 64;
     static constexpr uint32_t TMEM_COLS = 512 / CTAS;
@@ -57,7 +59,8 @@ struct FwMaps {
     CUtensorMap q, k, v;
 };
 
-constexpr int ERR_FW_LOAD = 0x201, ERR_FW_MMA = 0x202, ERR_FW_SOFTMAX = 0x203, ERR_FW_ALIGN = 0x204;
+constexpr int ERR_FW_LOAD = 0x201, ERR_FW_MMA = 0x202, ERR_FW_SOFTMAX = 0x203, ERR_FW_ALIGN = 0x204,
+              ERR_FW_CLEAN = 0x205;
 
 // Raises *addr to v.  Signed order of the bits is the order of non-negative floats, the
 // reverse unsigned order that of negative ones.
@@ -65,6 +68,32 @@ __device__ __forceinline__ void atomic_max_float(float* addr, float v) {
     v += 0.f;                                   // -0 counts as +0
     if (v >= 0.f) atomicMax(reinterpret_cast<int*>(addr), __float_as_int(v));
     else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(addr), __float_as_uint(v));
+}
+
+// Gives a row the infinities and NaN of V that the products did without: those of the keys from
+// `first`, the first that a row of the CTA does not see, up to the last one it sees itself.  A
+// key whose values the products had as well gives the same again.
+template <int DP>
+__device__ __noinline__ void add_nonfinite(const AttnParams& p, uint32_t o_t, int first, int last, bool live, int kv_head) {
+#pragma unroll 1
+    for (int i = 0; i < DP / 32; ++i) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_t + 32u * i, o);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int j = first; live && j <= last; ++j) {
+            const __nv_bfloat16* v = p.v.p + (long long)j * p.v.rs + (long long)kv_head * p.v.hs + 32 * i;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (32 * i + e < p.d) {
+                    const float x = __bfloat162float(v[e]);
+                    if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                }
+        }
+        __syncwarp();
+        tmem_st_32x32b_x32(o_t + 32u * i, o);
+    }
+    tmem_st_wait();
 }
 
 template <int DP>
@@ -87,10 +116,13 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     uint64_t* p_ready = s_read + TILES;         // two: for each half of the keys
     uint64_t* pv_done = p_ready + 2 * TILES;    // P has been read, O holds it
     uint64_t* o_full = pv_done + TILES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + TILES);
+    uint64_t* near = o_full + TILES;            // the next edge tile may be cleaned
+    uint64_t* clean = near + 1;                 // per edge tile: its V is fit for the product
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + L::EDGES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
-    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
+    volatile int* poisoned = reinterpret_cast<volatile int*>(tmem_slot + 3);      // infinities or NaN of V were set to zero
+    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
 
     const uint32_t warp = warp_id();
     const int head = (int)(blockIdx.x % (unsigned)p.hq);
@@ -124,6 +156,9 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             mbar_init(&o_full[i], 1);
         }
         *abort_flag = 0;
+        *poisoned = 0;
+        mbar_init(near, 1);
+        for (int i = 0; i < L::EDGES; ++i) mbar_init(&clean[i], L::CLEANERS);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -146,85 +181,111 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
         }
         const int nmax = max(n[0], n[TILES - 1]), nmin = min(n[0], n[TILES - 1]);
 
-        if (warp == L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && nmax > 0) {
-                mbar_arrive_expect_tx(q_full, TILES * L::TILE);
-                for (int w = 0; w < TILES; ++w)
-                    load_tile<DP, AT_ROWS, AT_ROWS>(sq + w * L::TILE, &maps.q, q_full, head, q0 + row0 + w * AT_ROWS);
-                // ring order: K0, K1, V0, K2, V1, ...: the order of use
-                int slot = 0;
-                uint32_t phase = 0;
-                bool ok = true;
-                for (int i = 0; i < 2 * nmax && ok; ++i) {
-                    const bool is_v = i > 0 && (i % 2 == 0 || i == 2 * nmax - 1);
-                    const int j = i == 0 ? 0 : is_v ? (i == 2 * nmax - 1 ? nmax - 1 : i / 2 - 1) : (i + 1) / 2;
-                    if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err, ERR_FW_LOAD)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[slot], L::TILE);
-                    load_tile<DP, AT_ROWS, AT_ROWS>(ring + slot * L::TILE, is_v ? &maps.v : &maps.k, &full[slot], kv_head,
-                                                    k0 + j * AT_ROWS);
-                    if (++slot == L::SLOTS) { slot = 0; phase ^= 1u; }
-                }
-                // every load has landed before the CTA may end
-                for (int i = 0; i < L::SLOTS && ok; ++i) {
-                    if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err, ERR_FW_LOAD)) ok = false;
-                    if (++slot == L::SLOTS) { slot = 0; phase ^= 1u; }
-                }
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
-            }
-        } else if (warp == L::W_MMA || warp == L::W_MMA + TILES - 1) {
-            regs_less<L::REGS_OTHER>();
-            if (elect_one() && nmax > 0) {
-                const int w = (int)warp - L::W_MMA, nw = n[w], kw = keys[w];
-                bool ok = mbar_wait(q_full, 0, abort_flag, p.err, ERR_FW_MMA);
-                const uint32_t q_s = smem_u32(sq) + w * L::TILE, ring_s = smem_u32(ring);
-                const uint32_t s_t = tmem + L::S_COL + 128u * w, p_t = tmem + L::P_COL + 128u * w,
-                               o_t = tmem + L::O_COL + (uint32_t)(DP * w);
-                // ring position of K_j and V_j
-                auto k_at = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-                auto v_at = [&](int j) { return j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2; };
-                auto wait_full = [&](int at) {
-                    return mbar_wait(&full[at % L::SLOTS], (uint32_t)(at / L::SLOTS) & 1u, abort_flag, p.err, ERR_FW_MMA);
-                };
-                auto tile_s = [&](int at) { return ring_s + (uint32_t)(at % L::SLOTS) * L::TILE; };
-                auto do_s = [&](int j) {
-                    if (!wait_full(k_at(j))) return false;
-                    tc_fence_after();
-                    mma_abt<DP, AT_ROWS>(s_t, q_s, tile_s(k_at(j)));
-                    tc_commit(&s_full[w]);
-                    tc_commit(&empty[k_at(j) % L::SLOTS]);
-                    return true;
-                };
-                if (nw > 0) ok = ok && do_s(0);
-                for (int j = 0; j < nw && ok; ++j) {
-                    if (L::P_APART && j + 1 < nw)
-                        ok = mbar_wait(&s_read[w], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA) && do_s(j + 1);
-                    ok = ok && wait_full(v_at(j));
-                    // a last tile of 64 keys at most leaves its upper half out
-                    const int halves = kw - j * AT_ROWS > 64 ? 2 : 1;
-                    for (int h = 0; h < halves && ok; ++h) {
-                        if (!(ok = mbar_wait(&p_ready[2 * w + h], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA))) break;
-                        tc_fence_after();
-                        mma_tb_half<DP>(o_t, p_t + L::P_HALF * h, tile_s(v_at(j)), h, j > 0 || h > 0);
+        // Key tiles from this one on hold keys that some row does not see.
+        const int edge0 = max(0, row0 + shift + 1) / AT_ROWS;
+
+        if (warp >= L::W_TMA) {
+            regs_less<L::REGS_OTHER>();     // one instruction for all warps of the group
+            if (warp == L::W_TMA) {
+                if (elect_one() && nmax > 0) {
+                    mbar_arrive_expect_tx(q_full, TILES * L::TILE);
+                    for (int w = 0; w < TILES; ++w)
+                        load_tile<DP, AT_ROWS, AT_ROWS>(sq + w * L::TILE, &maps.q, q_full, head, q0 + row0 + w * AT_ROWS);
+                    // ring order: K0, K1, V0, K2, V1, ...: the order of use
+                    int slot = 0;
+                    uint32_t phase = 0;
+                    bool ok = true;
+                    for (int i = 0; i < 2 * nmax && ok; ++i) {
+                        const bool is_v = i > 0 && (i % 2 == 0 || i == 2 * nmax - 1);
+                        const int j = i == 0 ? 0 : is_v ? (i == 2 * nmax - 1 ? nmax - 1 : i / 2 - 1) : (i + 1) / 2;
+                        if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err, ERR_FW_LOAD)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&full[slot], L::TILE);
+                        load_tile<DP, AT_ROWS, AT_ROWS>(ring + slot * L::TILE, is_v ? &maps.v : &maps.k, &full[slot], kv_head,
+                                                        k0 + j * AT_ROWS);
+                        if (++slot == L::SLOTS) { slot = 0; phase ^= 1u; }
                     }
+                    // every load has landed before the CTA may end
+                    for (int i = 0; i < L::SLOTS && ok; ++i) {
+                        if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err, ERR_FW_LOAD)) ok = false;
+                        if (++slot == L::SLOTS) { slot = 0; phase ^= 1u; }
+                    }
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);
+                }
+            } else if (warp == L::W_MMA || warp == L::W_MMA + TILES - 1) {
+                if (elect_one() && nmax > 0) {
+                    const int w = (int)warp - L::W_MMA, nw = n[w], kw = keys[w];
+                    bool ok = mbar_wait(q_full, 0, abort_flag, p.err, ERR_FW_MMA);
+                    const uint32_t q_s = smem_u32(sq) + w * L::TILE, ring_s = smem_u32(ring);
+                    const uint32_t s_t = tmem + L::S_COL + 128u * w, p_t = tmem + L::P_COL + 128u * w,
+                                   o_t = tmem + L::O_COL + (uint32_t)(DP * w);
+                    // ring position of K_j and V_j
+                    auto k_at = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+                    auto v_at = [&](int j) { return j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2; };
+                    auto wait_full = [&](int at) {
+                        return mbar_wait(&full[at % L::SLOTS], (uint32_t)(at / L::SLOTS) & 1u, abort_flag, p.err, ERR_FW_MMA);
+                    };
+                    auto tile_s = [&](int at) { return ring_s + (uint32_t)(at % L::SLOTS) * L::TILE; };
+                    auto do_s = [&](int j) {
+                        if (!wait_full(k_at(j))) return false;
+                        tc_fence_after();
+                        mma_abt<DP, AT_ROWS>(s_t, q_s, tile_s(k_at(j)));
+                        tc_commit(&s_full[w]);
+                        tc_commit(&empty[k_at(j) % L::SLOTS]);
+                        return true;
+                    };
+                    // A V tile may be cleaned from the tile before on: what its slot held then has been waited for.
+                    const bool leads = w == (n[0] == nmax ? 0 : TILES - 1);
+                    if (leads && edge0 == 0) mbar_arrive(near);
+                    if (nw > 0) ok = ok && do_s(0);
+                    for (int j = 0; j < nw && ok; ++j) {
+                        if (L::P_APART && j + 1 < nw)
+                            ok = mbar_wait(&s_read[w], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA) && do_s(j + 1);
+                        ok = ok && wait_full(v_at(j));
+                        if (j >= edge0) ok = ok && mbar_wait(&clean[j - edge0], 0, abort_flag, p.err, ERR_FW_MMA);
+                        if (leads && j + 1 >= edge0 && j + 1 < nw) mbar_arrive(near);
+                        // a last tile of 64 keys at most leaves its upper half out
+                        const int halves = kw - j * AT_ROWS > 64 ? 2 : 1;
+                        for (int h = 0; h < halves && ok; ++h) {
+                            if (!(ok = mbar_wait(&p_ready[2 * w + h], (uint32_t)j & 1u, abort_flag, p.err, ERR_FW_MMA))) break;
+                            tc_fence_after();
+                            mma_tb_half<DP>(o_t, p_t + L::P_HALF * h, tile_s(v_at(j)), h, j > 0 || h > 0);
+                        }
+                        if (!ok) break;
+                        tc_commit(&pv_done[w]);
+                        tc_commit(&empty[v_at(j) % L::SLOTS]);
+                        if (j + 1 == nw) tc_commit(&o_full[w]);
+                        // S takes P's place: products run in order, so P V has read it
+                        if (!L::P_APART && j + 1 < nw) ok = do_s(j + 1);
+                    }
+                    // a tile that is done still passes the other one's K and V on, once they have arrived
+                    for (int at = nw == 0 ? 0 : 2 * nw - 1; at < 2 * nmax && ok; ++at) {
+                        if (nw > 0 && nw < nmax && at == 2 * nw) continue;      // V of its last tile
+                        if (nw > 0 && nw == nmax) break;
+                        ok = wait_full(at);
+                        if (ok) mbar_arrive(&empty[at % L::SLOTS]);
+                    }
+                    if (!ok || *abort_flag) spin_ns_at_most(2000000ull);    // products in flight end
+                }
+            } else if (warp >= L::W_CLEAN && warp <= L::W_TMEM) {
+                // P is 0 for keys that a row does not see, but 0 times V need not be: rows behind the sequence's keys
+                // become zero, as do infinities and NaN of keys that some row does not see (add_nonfinite gives them
+                // back to the rows that do).  Done here while the tile's softmax runs.
+                const int lane = (int)threadIdx.x - 32 * L::W_CLEAN;
+                bool ok = true;
+                for (int j = edge0; j < nmax && ok; ++j) {
+                    const int at = j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2, key0 = j * AT_ROWS;
+                    ok = mbar_wait(near, (uint32_t)(j - edge0) & 1u, abort_flag, p.err, ERR_FW_CLEAN) &&
+                         mbar_wait(&full[at % L::SLOTS], (uint32_t)(at / L::SLOTS) & 1u, abort_flag, p.err, ERR_FW_CLEAN);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    tc_commit(&pv_done[w]);
-                    tc_commit(&empty[v_at(j) % L::SLOTS]);
-                    if (j + 1 == nw) tc_commit(&o_full[w]);
-                    // S takes P's place: products run in order, so P V has read it
-                    if (!L::P_APART && j + 1 < nw) ok = do_s(j + 1);
+                    const uint32_t v_s = smem_u32(ring + (at % L::SLOTS) * L::TILE);
+                    if (lk - key0 < AT_ROWS) zero_rows<DP>(v_s, lk - key0, AT_ROWS, lane, 32 * L::CLEANERS);
+                    if (clean_rows<DP>(v_s, max(0, row0 + shift + 1 - key0), AT_ROWS, min(AT_ROWS, lk - key0), lane, 32 * L::CLEANERS)) *poisoned = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(&clean[j - edge0]);
                 }
-                // a tile that is done still passes the other one's K and V on, once they have arrived
-                for (int at = nw == 0 ? 0 : 2 * nw - 1; at < 2 * nmax && ok; ++at) {
-                    if (nw > 0 && nw < nmax && at == 2 * nw) continue;      // V of its last tile
-                    if (nw > 0 && nw == nmax) break;
-                    ok = wait_full(at);
-                    if (ok) mbar_arrive(&empty[at % L::SLOTS]);
-                }
-                if (!ok || *abort_flag) spin_ns_at_most(2000000ull);    // products in flight end
             }
-        } else if (warp >= L::W_TMA) {
-            regs_less<L::REGS_OTHER>();
         } else {
             regs_more<L::REGS_SOFTMAX>();
             const int w = (int)(warp >> 2), t = (int)(threadIdx.x & 127u);
@@ -296,13 +357,6 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                         }
                     }
                 }
-                if (lk - key0 < AT_ROWS) {
-                    // rows behind the sequence's keys: P is 0 there, but 0 times what lies behind need not be
-                    const int at = j == nmax - 1 ? 2 * nmax - 1 : 2 * j + 2;
-                    wait(&full[at % L::SLOTS], at / L::SLOTS);
-                    zero_rows<DP>(smem_u32(ring + (at % L::SLOTS) * L::TILE), lk - key0, AT_ROWS, t, 128);
-                    fence_proxy_async_smem();
-                }
                 const float base = m == -INFINITY ? 0.f : m * c;
                 const uint64_t c2 = pack2(c, c), b2 = pack2(-base, -base);
                 uint64_t sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
@@ -346,6 +400,8 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 const bool live = row < lq;
                 // no key seen: the sum is 0, or some 2^-126 from exp2_pair
                 const bool none = m == -INFINITY && l == l;
+                if (nw > 0 && __any_sync(0xffffffffu, *poisoned != 0))
+                    add_nonfinite<DP>(p, o_t, k0 + max(0, row0 + shift + 1), k0 + see, live, kv_head);
                 const float inv = none ? 0.f : 1.f / l;
                 for (int h = 0; h < 2; ++h)
                     store_rows<DP>(o_t + (uint32_t)(DP / 2 * h), nw > 0, none, inv, smem_u32(sq) + w * L::TILE, h,

@@ -193,6 +193,56 @@ def test_one_sequence_never_reaches_another(opt, bad):
     assert torch.equal(got[1][:, :100], want[1][:, :100]) and torch.equal(got[1][:, 177:], want[1][:, 177:])
 
 
+@pytest.mark.parametrize("hq,hk,d", [(2, 1, 128), (2, 2, 64)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("at", [0, 63, 100, 200, 299])
+def test_later_tokens_never_reach_earlier_ones(opt, at, bad, hq, hk, d):
+    """A non-finite value of v, or of all of token `at`, reaches the queries from `at` on and no earlier one, bit for
+    bit; those from `at` on show it."""
+    q, k, v, do = inputs(30 + at, 300, 300, hq, hk, d)
+    want = [t.clone() for t in run_both(opt, q, k, v, do, cu([300]), cu([300]))]
+    v2 = v.clone()
+    v2[at, 0, 3] = bad
+    out, lse = opt.attention(q, k, v2, cu([300]))
+    opt.sync()
+    assert torch.equal(out[:at], want[0][:at]) and torch.equal(lse, want[1])
+    assert not bool(torch.isfinite(out[at:, 0, 3]).any())
+    assert torch.equal(out[:, :, 4:], want[0][:, :, 4:]) and torch.equal(out[:, :, :3], want[0][:, :, :3])
+    for t in (q, k, v):
+        t[at] = bad
+    got = run_both(opt, q, k, v, do, cu([300]), cu([300]))
+    assert torch.equal(got[0][:at], want[0][:at]) and torch.equal(got[1][:, :at], want[1][:, :at])
+    assert torch.equal(got[3][:at], want[3][:at])
+    assert not bool(torch.isfinite(got[0][at]).any()) and not bool(torch.isfinite(got[3][at:]).any())
+
+
+@pytest.mark.parametrize("hq,hk,d", [(2, 1, 128), (2, 2, 64)])
+@pytest.mark.parametrize("at", [0, 70, 128, 299])
+def test_gradients_of_keys_that_a_bad_query_does_not_see(opt, at, hq, hk, d):
+    """A non-finite output gradient of query `at` reaches its dq and the keys up to `at`, and nothing else."""
+    q, k, v, do = inputs(60 + at, 300, 300, hq, hk, d)
+    want = [t.clone() for t in run_both(opt, q, k, v, do, cu([300]), cu([300]))]
+    for bad in (math.nan, math.inf):
+        do[at] = bad
+        got = run_both(opt, q, k, v, do, cu([300]), cu([300]))
+        for i in (4, 5):
+            assert torch.equal(got[i][at + 1:], want[i][at + 1:]), i
+        assert not bool(torch.isfinite(got[5][:at + 1]).any())
+        keep = torch.arange(300, device="cuda") != at
+        assert torch.equal(got[3][keep], want[3][keep])
+
+
+def test_single_tokens_have_no_gradient_but_dv(opt):
+    """A query that sees one key has P = 1: its out is v, and dq and dk are zero exactly."""
+    for d, hq, hk in ((64, 4, 2), (128, 2, 2)):
+        n = 140
+        q, k, v, do = inputs(90 + d, n, n, hq, hk, d)
+        out, lse, top, dq, dk, dv = run_both(opt, q, k, v, do, cu([1] * n), cu([1] * n))
+        assert torch.equal(out, v.repeat_interleave(hq // hk, 1)) and not dq.any() and not dk.any()
+        want = do.float().view(n, hk, -1, d).sum(2)
+        assert float((dv.float() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max())
+
+
 def test_views_of_one_fused_projection(opt):
     """q, k, v (and dq, dk, dv) as strided views of one array, and heads-first arrays: the same bits as dense ones."""
     ql, hq, hk, d = [150, 3, 260], 6, 2, 64
