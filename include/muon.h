@@ -278,7 +278,7 @@ typedef struct {
  * statistics and products are accumulated in fp32; the exponentials enter the second
  * product rounded to bf16.
  *
- * head_dim: a multiple of 8, at most 128.  scale: finite and > 0.  q, k, v: read; out:
+ * head_dim: a multiple of 8, at most 128.  scale: 2^-64 to 2^64.  q, k, v: read; out:
  * written; lse: fp32 [n_heads][total_q], written; max_logits: n_heads floats or NULL,
  * updated in place (start an optimizer step's micro-batches from -inf; a NaN logit is
  * passed over with its row).  out, lse and max_logits may not overlap any buffer of the call
@@ -286,7 +286,8 @@ typedef struct {
  * Non-finite values reach the outputs of the queries that see them and no others: not
  * those of earlier queries, nor of another sequence.
  * cu_seqlens values outside the rule above are seen by the kernels only: such a
- * sequence is passed over, and muon_sync reports MUON_ERR_INVALID. */
+ * sequence is passed over (with more than 64 sequences others may be, too), and
+ * muon_sync reports MUON_ERR_INVALID. */
 typedef struct {
     int n_seqs, n_heads, n_kv_heads, head_dim;
     int total_q, total_k;            /* rows of q / out / lse and of k / v */
@@ -300,7 +301,7 @@ typedef struct {
 } muon_attention_args;
 
 /* Host-only check, usable without a GPU.  MUON_OK, MUON_ERR_INVALID or
- * MUON_ERR_UNSUPPORTED (a head_dim or alignment that the kernels do not take). */
+ * MUON_ERR_UNSUPPORTED (a head_dim, scale or alignment that the kernels do not take). */
 muon_status muon_validate_attention(const muon_attention_args* args);
 muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void* stream);
 
@@ -315,8 +316,8 @@ muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void
  * grad_out: layout of out; dq, dk, dv: layouts of q, k, v, written (rows of no
  * sequence are not; keys that no query sees get zero).  delta: scratch for
  * n_heads * total_q floats, written.  P and dS enter their products rounded to bf16.
- * A query with a non-finite value of its own, or that sees one, makes its dq NaN, and dk
- * and dv of the keys that it sees; no other gradient of the call.
+ * Non-finite values of a query, or that a query sees, reach its dq and the dk and dv of
+ * the keys that it sees, and no other gradient.
  * dq, dk, dv and delta may not overlap any buffer of the call. */
 typedef struct {
     muon_attention_args forward;

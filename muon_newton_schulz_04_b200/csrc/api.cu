@@ -360,6 +360,8 @@ muon_status check_attention(const muon_attention_args* a, bool forward, Extent* 
     }
     if (a->n_heads % a->n_kv_heads != 0) { *why = "n_heads must be a multiple of n_kv_heads"; return MUON_ERR_INVALID; }
     if (!(finite(a->scale) && a->scale > 0.f)) { *why = "scale must be finite and > 0"; return MUON_ERR_INVALID; }
+    // lse / scale and scale * log2(e) are formed in fp32
+    if (a->scale < 0x1p-64f || a->scale > 0x1p64f) { *why = "scale must be in 2^-64 .. 2^64"; return MUON_ERR_UNSUPPORTED; }
     if (a->head_dim % 8 != 0 || a->head_dim > 128) { *why = "head_dim must be a multiple of 8, at most 128"; return MUON_ERR_UNSUPPORTED; }
     if (a->n_heads > 32768 || a->n_seqs > (1 << 24) || a->total_q > (1 << 30) || a->total_k > (1 << 30) ||
         ((long long)a->total_q / 128 + a->n_seqs + 1) * a->n_heads > (1ll << 31) - 1 ||

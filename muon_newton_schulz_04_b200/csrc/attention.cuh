@@ -17,45 +17,76 @@ struct SeqTile {
     int q0, lq, k0, lk, block, blocks;
 };
 
-// The block with index `t` when the sequences' blocks of `rows` query (or key) rows are
-// counted in order; called by a whole warp, false when t is past the last one.  Sequences
-// whose bounds are out of range count as empty; with check_all every sequence is looked at
-// and a bad one reported.
-__device__ __forceinline__ bool find_tile(const AttnParams& p, bool by_key, int rows, int t, bool check_all, SeqTile& r) {
+// Bounds of sequence s, all 0 when they are out of range.
+__device__ __forceinline__ bool seq_bounds(const AttnParams& p, int s, int& q0, int& q1, int& k0, int& k1) {
+    q0 = p.cu_q[s];
+    q1 = p.cu_q[s + 1];
+    k0 = p.cu_k[s];
+    k1 = p.cu_k[s + 1];
+    if (q0 >= 0 && q0 <= q1 && q1 <= p.total_q && k0 >= 0 && k0 <= k1 && k1 <= p.total_k) return true;
+    q0 = q1 = k0 = k1 = 0;
+    return false;
+}
+
+// Numbers that find_tile gives blocks are below this.
+__host__ __device__ __forceinline__ unsigned seq_blocks(int total, int rows, int n_seqs) { return (unsigned)(total / rows + n_seqs); }
+
+// The block of `rows` query (or key) rows with number `t`; called by a whole warp, false when
+// there is none.  Sequences whose bounds are out of range count as empty, and are reported:
+// CTA 0 looks at all of up to 64 sequences, else CTA c at those from 32 c on.
+//
+// Up to 64 sequences: blocks are numbered in order, two looks of the warp at most.  More:
+// those of sequence s from cu[s] / rows + s on, which is at or behind the end of the sequence
+// before; a search finds them without a sum over all sequences, but CTAs without a block lie
+// between the others (and bounds out of order may lead it past good sequences).  Forward pass
+// of 12 heads of 64: 64 sequences of 128 tokens 21.4 us in order, 23.8 by the search; 256 of
+// 128 109 and 89; 4096 of 16 3950 and 1010.
+constexpr int AT_IN_ORDER = 64;
+
+__device__ __forceinline__ bool find_tile(const AttnParams& p, bool by_key, int rows, int t, unsigned cta, SeqTile& r) {
     const int lane = (int)(threadIdx.x & 31u);
-    int before = 0;
+    const bool in_order = p.n_seqs <= AT_IN_ORDER;
+    int lo = 0, hi = p.n_seqs, before = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    if (!in_order) {
+        const long long s = 32ll * cta + lane;
+        if (s < p.n_seqs && !seq_bounds(p, (int)s, q0, q1, k0, k1)) atomicCAS(p.err, 0, ERR_SEQLENS);
+        const int* cu = by_key ? p.cu_k : p.cu_q;
+        while (hi - lo > 32) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const unsigned from = __ballot_sync(0xffffffffu, at < hi && max(cu[min(at, hi - 1)], 0) / rows + at <= t);
+            if (from == 0) return false;
+            lo += (__popc(from) - 1) * step;
+            hi = min(hi, lo + step);
+        }
+    }
     bool found = false;
-    for (int s0 = 0; s0 < p.n_seqs && (!found || check_all); s0 += 32) {
-        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-        if (s0 + lane < p.n_seqs) {
-            q0 = p.cu_q[s0 + lane];
-            q1 = p.cu_q[s0 + lane + 1];
-            k0 = p.cu_k[s0 + lane];
-            k1 = p.cu_k[s0 + lane + 1];
-            if (!(q0 >= 0 && q0 <= q1 && q1 <= p.total_q && k0 >= 0 && k0 <= k1 && k1 <= p.total_k)) {
-                if (check_all) atomicCAS(p.err, 0, ERR_SEQLENS);
-                q0 = q1 = k0 = k1 = 0;
-            }
-        }
+    for (; lo < hi && (!found || (in_order && cta == 0)); lo += 32) {
+        const int s = lo + lane;
+        q0 = q1 = k0 = k1 = 0;
+        if (s < hi && !seq_bounds(p, s, q0, q1, k0, k1) && in_order && cta == 0) atomicCAS(p.err, 0, ERR_SEQLENS);
         const int n = ((by_key ? k1 - k0 : q1 - q0) + rows - 1) / rows;
-        int end = n;
+        int first = (by_key ? k0 : q0) / rows + s;
+        if (in_order) {
+            int end = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += v;
+            }
+            first = before + end - n;
+            before += __shfl_sync(0xffffffffu, end, 31);
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + end > t);
-        if (!found && past != 0) {
-            const int l = __ffs((int)past) - 1;
+        const unsigned in = __ballot_sync(0xffffffffu, t >= first && t - first < n);
+        if (!found && in != 0) {
+            const int l = __ffs((int)in) - 1;
             r.q0 = __shfl_sync(0xffffffffu, q0, l);
             r.lq = __shfl_sync(0xffffffffu, q1, l) - r.q0;
             r.k0 = __shfl_sync(0xffffffffu, k0, l);
             r.lk = __shfl_sync(0xffffffffu, k1, l) - r.k0;
             r.blocks = __shfl_sync(0xffffffffu, n, l);
-            r.block = t - (before + __shfl_sync(0xffffffffu, end, l) - r.blocks);
+            r.block = t - __shfl_sync(0xffffffffu, first, l);
             found = true;
         }
-        before += __shfl_sync(0xffffffffu, end, 31);
     }
     return found;
 }

@@ -108,7 +108,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     pdl_trigger();          // after the wait: the second kernel starts on what came before this one
     if (warp == 0) {
         SeqTile t;
-        const bool ok = find_tile(p, false, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x == 0, t);
+        const bool ok = find_tile(p, false, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x, t);
         if (elect_one()) {
             *found = ok;
             info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
@@ -427,7 +427,7 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     if (warp == 0) {
         SeqTile t;
         // first blocks of a sequence first: most queries see them
-        const bool ok = find_tile(p, true, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hk), blockIdx.x == 0, t);
+        const bool ok = find_tile(p, true, AT_ROWS, (int)(blockIdx.x / (unsigned)p.hk), blockIdx.x, t);
         if (elect_one()) {
             *found = ok;
             info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
@@ -738,9 +738,6 @@ attention_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     }
 }
 
-// Blocks of 128 rows of up to n_seqs sequences: at most one partial block each.
-unsigned most_tiles(int total, int n_seqs) { return (unsigned)(total / AT_ROWS + std::min(n_seqs, total)); }
-
 template <int DP>
 cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) {
     using L = BwLayout<DP>;
@@ -755,7 +752,7 @@ cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) 
     }();
     if (regs < L::REGS) return cudaErrorInvalidConfiguration;
     if (p.total_q > 0) {
-        e = launch_pdl(attention_dq_kernel<DP>, dim3(most_tiles(p.total_q, p.n_seqs) * (unsigned)p.hq), dim3(L::THREADS),
+        e = launch_pdl(attention_dq_kernel<DP>, dim3(seq_blocks(p.total_q, AT_ROWS, p.n_seqs) * (unsigned)p.hq), dim3(L::THREADS),
                        DqLayout<DP>::SMEM, s, p, maps);
         if (e != cudaSuccess) return e;
     }
@@ -763,10 +760,10 @@ cudaError_t launch_bwd(const AttnParams& p, const BwMaps& maps, cudaStream_t s) 
     // (without queries the kernel before is another one's, and its CTAs wait for nothing they read: cu_seqlens
     // and the zeros they write come after a plain launch)
     if (p.total_q == 0) {
-        attention_dkv_kernel<DP><<<most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk, L::THREADS, DkvLayout<DP>::SMEM, s>>>(p, maps);
+        attention_dkv_kernel<DP><<<seq_blocks(p.total_k, AT_ROWS, p.n_seqs) * (unsigned)p.hk, L::THREADS, DkvLayout<DP>::SMEM, s>>>(p, maps);
         return cudaGetLastError();
     }
-    return launch_pdl(attention_dkv_kernel<DP>, dim3(most_tiles(p.total_k, p.n_seqs) * (unsigned)p.hk), dim3(L::THREADS),
+    return launch_pdl(attention_dkv_kernel<DP>, dim3(seq_blocks(p.total_k, AT_ROWS, p.n_seqs) * (unsigned)p.hk), dim3(L::THREADS),
                       DkvLayout<DP>::SMEM, s, p, maps);
 }
 

@@ -130,7 +130,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
     pdl_wait();             // cu_seqlens, too, may be the previous kernel's
     if (warp == 0) {
         SeqTile t;
-        const bool ok = find_tile(p, false, TILES * AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x == 0, t);
+        const bool ok = find_tile(p, false, TILES * AT_ROWS, (int)(blockIdx.x / (unsigned)p.hq), blockIdx.x, t);
         if (elect_one()) {
             *found = ok;
             info[0] = make_int4(t.q0, t.lq, t.k0, t.lk);
@@ -439,8 +439,7 @@ cudaError_t launch_fwd(const AttnParams& p, const FwMaps& maps, cudaStream_t s) 
         return cudaFuncGetAttributes(&a, attention_fwd_kernel<DP>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs < L::REGS) return cudaErrorInvalidConfiguration;
-    // at most one partial block per sequence
-    const unsigned tiles = (unsigned)(p.total_q / (L::TILES * AT_ROWS) + std::min(p.n_seqs, p.total_q));
+    const unsigned tiles = seq_blocks(p.total_q, L::TILES * AT_ROWS, p.n_seqs);
     return launch_pdl(attention_fwd_kernel<DP>, dim3(tiles * (unsigned)p.hq), dim3(L::THREADS), L::SMEM, s, p, maps);
 }
 

@@ -14,6 +14,9 @@ lse and the largest logits are fp32 sums of at most 128 + 2^13 terms: 1e-5 absol
 logits of order 10 leaves 8 fp32 steps of 2^-20 each.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -353,6 +356,75 @@ def test_sequence_bounds_out_of_range_are_reported(opt):
         assert e.value.status == mb.MUON_ERR_INVALID
         opt.sync()
     assert bool((out[20:] != 7).any())
+
+
+@pytest.mark.parametrize("n", [33, 1000, 1100])
+def test_many_sequences(opt, n):
+    """More sequences than one look of a warp covers, empty and long ones among them."""
+    ql = [0 if i % 5 == 3 else 1 + i % 4 for i in range(n)]
+    kl = [x + i % 3 for i, x in enumerate(ql)]
+    ql[n // 2], kl[n // 2] = 300, 290
+    ql[n - 2], kl[n - 2] = 130, 257
+    q, k, v, do = inputs(31, sum(ql), sum(kl), 2, 1, 64)
+    got = run_both(opt, q, k, v, do, cu(ql), cu(kl))
+    want = reference(q, k, v, ql, kl, 0.125, do)
+    seen = torch.isfinite(want[1])
+    assert torch.equal(torch.isfinite(got[1]), seen)
+    assert float((got[1].double() - want[1])[seen].abs().max()) <= TOL_STAT
+    assert float((got[2].double() - want[2]).abs().max()) <= TOL_STAT
+    for x, y, tol, what in zip((got[0],) + got[3:], (want[0],) + want[3:], (TOL_OUT,) + (TOL_GRAD,) * 3, ("out", "dq", "dk", "dv")):
+        close(x, y, tol, what)
+
+
+def test_bad_bounds_among_many_are_reported(opt):
+    q, k, v, do = inputs(32, 400, 400, 2, 2, 64)
+    c = torch.arange(0, 401, 4, dtype=torch.int32, device="cuda")       # 100 sequences of 4
+    for at, bad in ((0, -1), (70, 100), (100, 401)):
+        b = c.clone()
+        b[at] = bad
+        opt.attention(q, k, v, b)
+        with pytest.raises(mb.MuonError) as e:
+            opt.sync()
+        assert e.value.status == mb.MUON_ERR_INVALID
+    opt.attention(q, k, v, c)
+    opt.sync()
+
+
+FIRST_CALLS = """
+import torch, muon_newton_schulz_04_b200 as mb
+o = mb.Muon(mb.config())
+q = torch.ones(70, 2, 64, device="cuda", dtype=torch.bfloat16)
+do = torch.full_like(q, 0.5)
+c = torch.tensor([0, 3, 70], dtype=torch.int32, device="cuda")
+W = torch.ones(128, 24, device="cuda"); top = torch.full((2,), 400.0, device="cuda")
+s = torch.cuda.Stream()
+s.wait_stream(torch.cuda.current_stream())
+g = torch.cuda.CUDAGraph()
+with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+    out, lse = o.attention(q, q, q, c)
+    grads = o.attention_backward(do, q, q, q, out, lse, c)
+    ck = o.checkpoint(q.view(70, 128))
+    back = o.checkpoint_load(ck)
+    G = o.weight_grad(do.view(70, 128), ck, torch.empty(128, 128, device="cuda"))
+    Wq, Wk = W.clone(), W.clone()
+    o.qk_clip_grouped(Wq, Wk, top, 64, 100.0)
+g.replay()
+torch.cuda.synchronize()
+o.sync()
+assert torch.equal(out, q) and torch.equal(back, q.view(70, 128))
+assert torch.equal(G, torch.full_like(G, 35.0))
+assert torch.equal(Wq, W * 0.5) and torch.equal(Wk, W * 0.5)
+assert float(grads[2].float().sum(0).sub(35.0).abs().max()) <= 35.0 * 2.0 ** -7
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every operator's first call in its process is a captured one."""
+    mbuild.build()
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
 
 
 def test_nothing_to_do(opt):

@@ -66,6 +66,12 @@ def test_attention_does_not_support(kw):
     assert check(attention(**kw)) == mb.MUON_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("scale,want", [(2.0 ** -64, mb.MUON_OK), (2.0 ** 64, mb.MUON_OK),
+                                        (2.0 ** -65, mb.MUON_ERR_UNSUPPORTED), (2.0 ** 65, mb.MUON_ERR_UNSUPPORTED)])
+def test_attention_scales(scale, want):
+    assert check(attention(scale=scale)) == want
+
+
 def grad(fwd=None, **kw):
     d = dict(forward=fwd if fwd is not None else attention(), grad_out=heads(6, 256, 64), dq=heads(7, 256, 64),
              dk=heads(8, 128, 64), dv=heads(9, 128, 64), delta=BASE + 10 * 0x10000000)
