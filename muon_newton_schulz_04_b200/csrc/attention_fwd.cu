@@ -17,6 +17,15 @@
 // long as the two products of a 128-wide head take, twice as long as those of a 64-wide one.
 // So a quarter of them is computed on the FMA pipe (exp2_pair), at 12 cycles a warp; the best
 // mix of the two gets to 7.5 where the unit alone gets to 8.6.
+//
+// One B200: 8192 rows in 5 sequences (the longest 6500), 32 heads over 8 of 128: 338 us at full
+// clocks, 1.05 PFLOP/s, tensor pipe 52 % and special function unit 45 % of the cycles.  8
+// sequences of 1024, 25 heads of 64: 66 us; a CTA has 4.5 key tiles there, and its start and end
+// take as long as they do.
+//
+// P is 0 where a row does not see a key, but 0 times an infinity or a NaN is not: a spare warp
+// takes those out of V in the tiles that not every row sees all of, beside the softmax, and what
+// it took out is added again at the end to the rows that see it (66 us against 65 without).
 #include <algorithm>
 
 #include "attention.cuh"
