@@ -265,6 +265,64 @@ def test_views_of_one_fused_projection(opt):
     assert torch.equal(grads, torch.cat(want[3:], 1))
 
 
+def test_offsets_past_32_bits(opt):
+    """All eight arrays are column ranges of one array whose rows lie 2^20 elements apart: the last row starts past
+    2^32 elements.  The same bits as from dense arrays."""
+    n, h, d = 4100, 2, 64
+    wide = torch.empty(n, 1 << 20, dtype=torch.bfloat16, device="cuda")
+    views = [wide[:, 128 * i:128 * i + 128].view(n, h, d) for i in range(8)]
+    q, k, v, do = inputs(33, n, n, h, h, d)
+    for x, y in zip(views, (q, k, v, do)):
+        x.copy_(y)
+    c = cu([3000, 1100])
+    out, lse = opt.attention(q, k, v, c)
+    dense = (out, *opt.attention_backward(do, q, k, v, out, lse, c))
+    _, lse2 = opt.attention(*views[:3], c, out=views[4])
+    opt.attention_backward(views[3], *views[:3], views[4], lse2, c, dq=views[5], dk=views[6], dv=views[7])
+    opt.sync()
+    assert torch.equal(lse, lse2)
+    for x, y in zip(views[4:], dense):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 2), (128, 2)])
+def test_a_long_sequence(opt, d, hq):
+    """40000 tokens: rows and keys picked from it, by the formulas (for keys with the call's own log-sums).  A row's sum
+    is 313 additions of tiles' sums: 313 * 2^-24 = 1.9e-5 if all were off by half a step in one direction; of random
+    sign they stay below a tenth of that, within TOL_STAT."""
+    n = 40000
+    q, k, v, do = inputs(34, n, n, hq, 1, d)
+    c, scale = cu([n]), d ** -0.5
+    out, lse = opt.attention(q, k, v, c)
+    dq, dk, dv = opt.attention_backward(do, q, k, v, out, lse, c)
+    opt.sync()
+    q, k, v, do = (x.double() for x in (q, k[:, 0], v[:, 0], do))
+    rows = [0, 1, 127, 128, 20001, n - 1]
+    keys = [0, 63, 64, 19999, n - 130, n - 1]
+    want = {"out": [], "dq": [], "dk": [], "dv": []}
+    for i in rows:
+        for h in range(hq):
+            s = scale * (k[:i + 1] @ q[i, h])
+            assert abs(float(torch.logsumexp(s, 0)) - float(lse[h, i])) <= TOL_STAT
+            p = torch.softmax(s, 0)
+            o, dp = p @ v[:i + 1], v[:i + 1] @ do[i, h]
+            a = float((do[i, h] * o).abs().sum())
+            want["out"].append((out[i, h], o, 0 * o))
+            want["dq"].append((dq[i, h], scale * (p * (dp - do[i, h] @ o)) @ k[:i + 1], scale * a * (p @ k[:i + 1].abs())))
+    delta = (do * out.double()).sum(2)
+    for j in keys:
+        gk = gv = 0
+        for h in range(hq):
+            p = torch.exp(scale * (q[j:, h] @ k[j]) - lse[h, j:].double())
+            gv = gv + p @ do[j:, h]
+            gk = gk + scale * (p * (do[j:, h] @ v[j] - delta[j:, h])) @ q[j:, h]
+        want["dk"].append((dk[j, 0], gk, 0 * gk))
+        want["dv"].append((dv[j, 0], gv, 0 * gv))
+    for what, tol in (("out", TOL_OUT), ("dq", TOL_GRAD), ("dk", TOL_GRAD), ("dv", TOL_GRAD)):
+        got, y, slack = (torch.stack([x[m] for x in want[what]]) for m in range(3))
+        close(got, (y, slack), tol, what)
+
+
 def test_max_logits_keep_the_largest(opt):
     """Micro-batches raise one running maximum; heads whose logits are all negative count too."""
     q, k, v, _ = inputs(12, 90, 90, 4, 4, 64)
@@ -433,6 +491,23 @@ def test_nothing_to_do(opt):
     opt.attention_backward(e, e, e, e, out, lse, cu([0]))
     opt.sync()
     assert out.shape == e.shape
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_side_is_empty(opt, d):
+    """Queries without any key row in the call, and keys without any query row."""
+    x = inputs(36, 5, 5, 2, 2, d)[0]
+    e = torch.empty(0, 2, d, dtype=torch.bfloat16, device="cuda")
+    c, none = cu([2, 3]), cu([0, 0])
+    top = torch.full((2,), -math.inf, device="cuda")
+    out, lse = opt.attention(x, e, e, c, cu_seqlens_k=none, max_logits=top)
+    dq, dk, dv = opt.attention_backward(x, x, e, e, out, lse, c, cu_seqlens_k=none)
+    assert not out.any() and not dq.any() and bool((lse == -math.inf).all()) and bool((top == -math.inf).all())
+    assert dk.shape == e.shape and dv.shape == e.shape
+    out, lse = opt.attention(e, x, x, none, cu_seqlens_k=c)
+    dq, dk, dv = opt.attention_backward(e, e, x, x, out, lse, none, cu_seqlens_k=c)
+    opt.sync()
+    assert out.shape == e.shape and not dk.any() and not dv.any()
 
 
 def test_refusals(opt):

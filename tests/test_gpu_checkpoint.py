@@ -167,6 +167,26 @@ def test_weight_grad_strides_and_no_tokens(opt):
     assert not G.any()
 
 
+def test_strides_past_32_bits(opt):
+    """Rows 2^20 elements apart, the last one past 2^32 elements: the same bits as from dense arrays."""
+    n = 4100
+    wide = torch.empty(n, 1 << 20, dtype=torch.bfloat16, device="cuda")
+    x, dy, back = wide[:, :200], wide[:, 256:356], wide[:, 512:712]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(35)
+    dense_x = torch.randn(n, 200, generator=gen, device="cuda").to(torch.bfloat16)
+    dense_dy = torch.randn(n, 100, generator=gen, device="cuda").to(torch.bfloat16)
+    x.copy_(dense_x)
+    dy.copy_(dense_dy)
+    a, b = opt.checkpoint(x), opt.checkpoint(dense_x)
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    opt.checkpoint_load(a, out=back)
+    assert torch.equal(back, opt.checkpoint_load(b))
+    G = [opt.weight_grad(y, a, torch.empty(100, 200, device="cuda")) for y in (dy, dense_dy)]
+    opt.sync()
+    assert torch.equal(*G)
+
+
 def test_weight_grad_same_bits_and_non_finite(opt):
     x = normal(3, 5000, 160, dtype=torch.bfloat16)
     dy = normal(4, 5000, 128, dtype=torch.bfloat16)
