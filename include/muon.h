@@ -368,7 +368,9 @@ typedef struct {
     size_t workspace_bytes;
 } muon_weight_grad_args;
 
-/* Host-only; the first also works with the pointers unset (workspace size of the shape). */
+/* Host-only.  The first looks at dy's address and stride alone besides the sizes: a dy off
+ * 16-byte addresses, or with a stride that is no multiple of 8 elements, needs room for a
+ * copy of it as well (dy = NULL counts as aligned). */
 muon_status muon_weight_grad_workspace(const muon_weight_grad_args* args, size_t* bytes);
 muon_status muon_validate_weight_grad(const muon_weight_grad_args* args);
 muon_status muon_weight_grad(muon_handle* h, const muon_weight_grad_args* args, void* stream);
