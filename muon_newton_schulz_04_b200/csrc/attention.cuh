@@ -315,12 +315,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // 2^x of two values on the FMA pipe, which has time to spare beside the special function unit:
 // x = n + f with n the nearest integer (Cody-Waite), 2^f by its minimax polynomial of degree 4
-// on [-1/2, 1/2] (Remez exchange; relative error 2.6e-6), times 2^n.  Below -126, -inf
-// included, the result is 2^-126; NaN stays NaN, +inf gives NaN.
+// on [-1/2, 1/2] (Remez exchange; relative error 2.6e-6), times 2^n.  Below -126.5, -inf
+// included, n is -127 and its factor's bit pattern that of 0, so that a masked logit has
+// weight 0 exactly, as from ex2; NaN stays NaN, +inf gives NaN.
 __device__ __forceinline__ void exp2_pair(uint64_t x2, float& a, float& b) {
     float x, y;
     unpack2(x2, x, y);
-    x2 = pack2(max_nan(x, -126.f), max_nan(y, -126.f));
+    x2 = pack2(max_nan(x, -127.f), max_nan(y, -127.f));
     constexpr float MAGIC = 12582912.f;         // 1.5 * 2^23: the sum's low bits are the nearest integer
     const uint64_t t2 = add2(x2, pack2(MAGIC, MAGIC));
     const uint64_t f2 = fma2(add2(t2, pack2(-MAGIC, -MAGIC)), pack2(-1.f, -1.f), x2);

@@ -23,9 +23,10 @@
 // sequences of 1024, 25 heads of 64: 66 us; a CTA has 4.5 key tiles there, and its start and end
 // take as long as they do.
 //
-// P is 0 where a row does not see a key, but 0 times an infinity or a NaN is not: a spare warp
-// takes those out of V in the tiles that not every row sees all of, beside the softmax, and what
-// it took out is added again at the end to the rows that see it (66 us against 65 without).
+// P is 0 where a row does not see a key (exp2_pair and ex2 both give 0 for -inf), but 0 times
+// an infinity or a NaN is not: a spare warp takes those out of V in the tiles that not every
+// row sees all of, beside the softmax, and what it took out is added again at the end to the
+// rows that see it (66 us against 65 without).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -407,7 +408,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
             }
             if (ok && row0 + w * AT_ROWS < lq) {
                 const bool live = row < lq;
-                // no key seen: the sum is 0, or some 2^-126 from exp2_pair
+                // no key seen, or none with any weight: the sum is 0
                 const bool none = m == -INFINITY && l == l;
                 if (nw > 0 && __any_sync(0xffffffffu, *poisoned != 0))
                     add_nonfinite<DP>(p, o_t, k0 + max(0, row0 + shift + 1), k0 + see, live, kv_head);

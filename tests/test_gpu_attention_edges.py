@@ -1,0 +1,49 @@
+"""Attention, its gradients and what reads their results, at the values and layouts where the formulas
+and the kernels can part: against the formulas in 64 bits, or bit for bit where the change must not be seen."""
+import math
+
+import pytest
+import torch
+
+import muon_newton_schulz_04_b200 as mb
+from test_gpu_attention import TOL_GRAD, TOL_OUT, TOL_STAT, close, cu, inputs, opt, reference, run_both  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+LARGE = 3.3e38          # finite in bf16; 2^-126 of it is 3.9
+
+
+@pytest.mark.parametrize("hq,hk,d", [(2, 1, 128), (2, 2, 64), (1, 1, 40)])
+@pytest.mark.parametrize("at", [1, 7, 63, 64, 100, 129, 200, 299])
+def test_large_values_of_later_tokens_weigh_nothing(opt, at, hq, hk, d):
+    """The weight of a key that a query does not see is 0, not a small number: finite values however large of tokens
+    from `at` on leave earlier rows bit for bit as they were, and exactly 0 where the values that they see are 0."""
+    q, k, v, _ = inputs(130 + at, 300, 300, hq, hk, d)
+    want, lse = opt.attention(q, k, v, cu([300]))
+    v[at:] = LARGE
+    v[at::2] *= -1
+    got, lse2 = opt.attention(q, k, v, cu([300]))
+    v[:at] = 0
+    none, _ = opt.attention(q, k, v, cu([300]))
+    opt.sync()
+    assert torch.equal(got[:at], want[:at]) and torch.equal(lse, lse2)
+    assert not none[:at].any()
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_weights_below_the_smallest_number_are_zero(opt, d):
+    """Every key but the first has a logit 1024 or more below it (q = 1, k = 64 and -64): a weight of 2^-1477, 0 in
+    any type of 32 bits whichever unit computes it.  Values of 3.3e38 behind such weights, and output gradients of
+    that size, give 0 exactly."""
+    n = 300
+    q = torch.ones(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k = torch.full_like(q, -64.0)
+    k[0] = 64
+    v = torch.full_like(q, LARGE)
+    v[0] = 0
+    out, lse = opt.attention(q, k, v, cu([n]))
+    opt.sync()
+    assert not out.any()
+    dq, dk, dv = opt.attention_backward(v, q, k, torch.zeros_like(v), out, lse, cu([n]))
+    opt.sync()
+    assert not dv[1:].any() and not dq.any() and not dk.any()
