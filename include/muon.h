@@ -280,8 +280,10 @@ typedef struct {
  *
  * head_dim: a multiple of 8, at most 128.  scale: 2^-64 to 2^64.  q, k, v: read; out:
  * written; lse: fp32 [n_heads][total_q], written; max_logits: n_heads floats or NULL,
- * updated in place (start an optimizer step's micro-batches from -inf; a NaN logit is
- * passed over with its row).  out, lse and max_logits may not overlap any buffer of the call
+ * updated in place (start an optimizer step's micro-batches from -inf; a logit of +inf
+ * counts, and a row with a NaN logit, unless another is +inf, is passed over).  A logit of
+ * -inf has weight 0; a query whose logits all are -inf gets O = 0 and lse = -inf.
+ * out, lse and max_logits may not overlap any buffer of the call
  * (strided views that interleave without sharing an element do not overlap).
  * Non-finite values reach the outputs of the queries that see them and no others: not
  * those of earlier queries, nor of another sequence.

@@ -344,7 +344,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     for (int e = 0; e < 8; ++e)
                         x8[e] = max3(x8[e], __uint_as_float(s[i / 32][i % 32 + 2 * e]),
                                      __uint_as_float(s[i / 32][i % 32 + 2 * e + 1]));
-                // (a NaN among the logits is passed over here, and makes the sum NaN)
+                // (a NaN among the logits is passed over here, and makes the sum NaN, as +inf does)
                 top = max3(max3(top, x8[0], x8[1]), max3(x8[2], x8[3], x8[4]), max3(x8[5], x8[6], x8[7]));
                 const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * c > 8.f;
                 if (L::P_APART && j > 0) {                          // the P before has been read
@@ -422,7 +422,8 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                     p.lse[(size_t)head * p.total_q + q0 + row] =
                         none ? -INFINITY : (m == -INFINITY ? 0.f : m * p.scale) + logf(l);
                 if (p.max_logits != nullptr) {
-                    float best = live && l == l ? top : -INFINITY;          // a row with a NaN is passed over
+                    // a row with a NaN logit is passed over; +inf counts, although its row's sum is NaN, too (inf - inf)
+                    float best = live && (l == l || top == INFINITY) ? top : -INFINITY;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
                     if ((t & 31) == 0 && best > -INFINITY) atomic_max_float(p.max_logits + head, best * p.scale);

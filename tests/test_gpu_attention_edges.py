@@ -47,3 +47,35 @@ def test_weights_below_the_smallest_number_are_zero(opt, d):
     dq, dk, dv = opt.attention_backward(v, q, k, torch.zeros_like(v), out, lse, cu([n]))
     opt.sync()
     assert not dv[1:].any() and not dq.any() and not dk.any()
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_infinite_logits_count(opt, d):
+    """A logit of +inf is the largest: finite q and k of 1e20 overflow.  One of -inf is none, and has weight 0; a row
+    with a NaN among its logits is passed over."""
+    n = 200
+    q, k, v, _ = inputs(140 + d, n, n, 3, 3, d)
+    q[:, :, 0] = k[:, :, 0] = 0
+    c = cu([n])
+    want = torch.full((3,), -math.inf, device="cuda")
+    plain, _ = opt.attention(q, k, v, c, max_logits=want)
+    # only the last row sees the last key; 0 times 1e20 leaves every other logit as it was
+    q[-1, :2, 0] = 1e20
+    k[-1, 0, 0] = 1e20
+    k[-1, 1, 0] = -1e20
+    q[-1, 2, 0] = math.nan
+    top = torch.full((3,), -math.inf, device="cuda")
+    out, lse = opt.attention(q, k, v, c, max_logits=top)
+    opt.sync()
+    assert float(top[0]) == math.inf
+    ro, rl, rt = reference(q[:, 1:2], k[:, 1:2], v[:, 1:2], [n], [n], d ** -0.5)
+    assert abs(float(top[1]) - float(rt)) <= TOL_STAT and abs(float(lse[1, -1]) - float(rl[0, -1])) <= TOL_STAT
+    close(out[:, 1:2], ro, TOL_OUT, "out")
+    _, _, rt = reference(q[:-1, 2:], k[:-1, 2:], v[:-1, 2:], [n - 1], [n - 1], d ** -0.5)
+    assert abs(float(top[2]) - float(rt)) <= TOL_STAT
+    assert torch.equal(out[:-1], plain[:-1])
+    # a larger finite maximum of an earlier call is raised, too
+    top = torch.full((3,), 1e30, device="cuda")
+    opt.attention(q, k, v, c, max_logits=top)
+    opt.sync()
+    assert top.tolist() == [math.inf, float(torch.tensor(1e30)), float(torch.tensor(1e30))]
