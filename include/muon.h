@@ -237,11 +237,14 @@ muon_status muon_qk_clip(muon_handle* h, float* Wq, float* Wk, const float* max_
  * reads key head h / (n_heads / n_kv_heads)).  With gamma_h = min(1, tau / max_logits[h]),
  * the rows of key head g are multiplied by kappa_g = sqrt(smallest gamma_h of its
  * group) and the rows of query head h by gamma_h / kappa_g, so that every logit of
- * head h scales by exactly gamma_h and the shared key rows by one factor.  With
- * n_kv_heads == n_heads it is muon_qk_clip.  Wq: fp32 (n_heads*head_dim) x cols, Wk:
- * fp32 (n_kv_heads*head_dim) x cols, both required, row-major, device, updated in
- * place; max_logits: n_heads floats, device (muon_attention writes them); a NaN
- * entry clips nothing; tau > 0. */
+ * head h scales by exactly gamma_h and the shared key rows by one factor.  Heads with
+ * gamma_h = 0 (max_logits[h] = +inf, or tau / max_logits[h] below the smallest float)
+ * are left out of the smallest unless all of the group are such (kappa_g = 0 then, and
+ * the group's rows become 0): their query rows become 0 and the group's other heads
+ * are clipped as without them.  With n_kv_heads == n_heads it is muon_qk_clip.
+ * Wq: fp32 (n_heads*head_dim) x cols, Wk: fp32 (n_kv_heads*head_dim) x cols, both
+ * required, row-major, device, updated in place; max_logits: n_heads floats, device
+ * (muon_attention writes them); a NaN entry clips nothing; tau > 0. */
 muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const float* max_logits, int n_heads,
                                  int n_kv_heads, int head_dim, int cols, float tau, void* stream);
 

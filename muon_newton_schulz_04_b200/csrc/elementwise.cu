@@ -641,20 +641,22 @@ __global__ void __launch_bounds__(EW_THREADS) qk_clip_kernel(float* __restrict__
 
 // Factor of one row of W_q (y = 0) or W_k (y = 1) of QK-Clip with grouped heads: with
 // g_h = min(1, tau / max_logits[h]) a key head's rows take the root of its group's
-// smallest g, a query head's rows g_h divided by that.
+// smallest g, a query head's rows g_h divided by that.  Heads with g = 0 (an infinite logit)
+// are left out of that minimum unless the whole group is such: their query rows become 0, and
+// a root of 0 would take the other heads' with them.
 __device__ __forceinline__ float grouped_clip_factor(const float* __restrict__ max_logits, int head, int group,
                                                      bool key, float tau) {
     const int base = key ? head * group : head / group * group;
-    float g_min = 1.f, g_own = 1.f;
+    float g_min = INFINITY, g_own = 1.f;
     for (int i = 0; i < group; ++i) {
         const float s = max_logits[base + i];
         const float g = s > tau ? tau / s : 1.f;
-        g_min = fminf(g_min, g);
+        if (g > 0.f) g_min = fminf(g_min, g);
         if (base + i == head) g_own = g;
     }
-    const float root = sqrtf(g_min);
+    const float root = g_min <= 1.f ? sqrtf(g_min) : 0.f;
     if (key) return root;
-    return root > 0.f ? g_own / root : 0.f;     // an infinite logit gives g = 0
+    return root > 0.f ? g_own / root : 0.f;
 }
 
 // A block takes CLIP_RUN consecutive elements of one head, whose rows lie one after the other;

@@ -79,3 +79,28 @@ def test_infinite_logits_count(opt, d):
     opt.attention(q, k, v, c, max_logits=top)
     opt.sync()
     assert top.tolist() == [math.inf, float(torch.tensor(1e30)), float(torch.tensor(1e30))]
+
+
+def test_clip_with_infinite_logits(opt):
+    """A head whose logits overflowed has gamma = 0: its query rows become 0, and the other heads that share its key
+    rows are clipped as without it.  Where every head of a group is like that, the key rows become 0 too, as in the
+    call of ungrouped heads.  Finite elements: at most 5 * 2^-23 off (four roundings of a factor, one of the product)."""
+    hq, hk, d, cols, tau = 8, 2, 16, 50, 100.0
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(150)
+    Wq, Wk = (torch.randn(h * d, cols, generator=gen, device="cuda") for h in (hq, hk))
+    top = torch.tensor([math.inf, 50.0, 400.0, 200.0] + [math.inf] * 4, device="cuda")
+    wq, wk = Wq.clone(), Wk.clone()
+    opt.qk_clip_grouped(wq, wk, top, d, tau)
+    opt.sync()
+    fq = torch.tensor([0, 2, 0.5, 1, 0, 0, 0, 0], dtype=torch.float64, device="cuda").repeat_interleave(d)[:, None]
+    fk = torch.tensor([0.5, 0], dtype=torch.float64, device="cuda").repeat_interleave(d)[:, None]
+    for got, old, f in ((wq, Wq, fq), (wk, Wk, fk)):
+        want = old.double() * f
+        assert bool(((got.double() - want).abs() <= 5 * 2.0 ** -23 * want.abs()).all())
+    a, b = Wq.clone(), Wq.clone()
+    opt.qk_clip_grouped(a, b, top, d, tau)
+    c, e = Wq.clone(), Wq.clone()
+    opt.qk_clip(c, e, top, d, tau)
+    opt.sync()
+    assert not a[4 * d:].any() and torch.equal(a == 0, c == 0) and torch.equal(b == 0, e == 0)
