@@ -322,7 +322,9 @@ muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void
  * sequence are not; keys that no query sees get zero).  delta: scratch for
  * n_heads * total_q floats, written.  P and dS enter their products rounded to bf16.
  * Non-finite values of a query, or that a query sees, reach its dq and the dk and dv of
- * the keys that it sees, and no other gradient.
+ * the keys that it sees, as the formulas carry them (a key with a logit of -inf has weight
+ * 0, and an infinite component of it reaches that component of dq alone), and no other
+ * gradient.
  * dq, dk, dv and delta may not overlap any buffer of the call. */
 typedef struct {
     muon_attention_args forward;

@@ -269,6 +269,34 @@ __device__ __forceinline__ bool clean_rows(uint32_t tile, int first, int rows_in
     return met;
 }
 
+// Gives a row's accumulator the infinities and NaN, times f, that the products did without:
+// those of the key rows of x from `first`, the first that a row of the CTA does not see, up to
+// the last one that this row sees.  A key whose values the products had as well gives the same
+// again.  Columns col .. col + 32 N - 1, at o_t in tensor memory; d: the head's width.
+template <int N>
+__device__ __noinline__ void add_nonfinite(const HeadView& x, int d, uint32_t o_t, int col, float f, int first, int last,
+                                           bool live, int kv_head) {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_t + 32u * i, o);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int j = first; live && j <= last; ++j) {
+            const __nv_bfloat16* v = x.p + (long long)j * x.rs + (long long)kv_head * x.hs + col + 32 * i;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (col + 32 * i + e < d) {
+                    const float y = __bfloat162float(v[e]);
+                    if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y * f);
+                }
+        }
+        __syncwarp();
+        tmem_st_32x32b_x32(o_t + 32u * i, o);
+    }
+    tmem_st_wait();
+}
+
 // ---------------------------------------------------------------- arithmetic
 
 __device__ __forceinline__ float ex2(float x) {

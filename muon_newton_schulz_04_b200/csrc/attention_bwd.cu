@@ -106,7 +106,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(exch + 256);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
-    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 3) + 15) & ~uintptr_t(15));
+    volatile int* poisoned = reinterpret_cast<volatile int*>(tmem_slot + 3);      // infinities or NaN of K were set to zero
+    int4* info = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
 
     const uint32_t warp = warp_id();
     const int head = (int)(blockIdx.x % (unsigned)p.hq);
@@ -139,6 +140,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         mbar_init(near, 1);                             // the next edge tile may be cleaned
         mbar_init(clean, 2);                            // its K is fit for dS K
         *abort_flag = 0;
+        *poisoned = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -222,8 +224,8 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 }
             } else if (warp >= L::W_TMEM && warp < L::W_TMEM + 2) {
                 // dS is 0 for keys that a row does not see, but 0 times K need not be: rows behind the sequence's keys
-                // become zero, as do infinities and NaN of keys that some row does not see (rows that see them have
-                // lse = NaN).  Done here, when S has read the tile, while dS is formed.
+                // become zero, as do infinities and NaN of keys that some row does not see (add_nonfinite gives them
+                // back to the rows that do).  Done here, when S has read the tile, while dS is formed.
                 const int lane = (int)threadIdx.x - 32 * L::W_TMEM;
                 bool ok = true;
                 for (int j = edge0; j < n && ok; ++j) {
@@ -234,7 +236,7 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     const uint32_t tile = smem_u32(s_k + (j % L::KS) * L::MOVING);
                     const int behind = lk - j * L::STEP;
                     if (behind < L::STEP) zero_rows<DP>(tile, behind, L::STEP, lane, 64);
-                    clean_rows<DP>(tile, max(0, row0 + shift + 1 - j * L::STEP), L::STEP, min(L::STEP, behind), lane, 64);
+                    if (clean_rows<DP>(tile, max(0, row0 + shift + 1 - j * L::STEP), L::STEP, min(L::STEP, behind), lane, 64)) *poisoned = 1;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (elect_one()) mbar_arrive(clean);
@@ -377,6 +379,11 @@ attention_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             }
             if (ok) {
                 if (half == 0 && live) p.delta[stat] = D + rest;
+                // a key with an infinity or NaN has a logit of -inf, which leaves dS = 0 and the product 0 * x, or one that
+                // makes lse NaN, and with it the whole row
+                if (n > 0 && __any_sync(0xffffffffu, *poisoned != 0))
+                    add_nonfinite<2 / L::HALVES>(p.k, p.d, tmem + lane_base + L::DQ_COL + 64u * half, 64 * half, 0.f,
+                                                 k0 + max(0, row0 + shift + 1), k0 + row + shift, live, kv_head);
                 for (int h = half; h < 2; h += L::HALVES)
                     store_rows<DP>(tmem + lane_base + L::DQ_COL + (uint32_t)(h * (DP / 2)), n > 0, n == 0, p.scale,
                                    smem_u32(s_q), h, (int)(warp & 3u) * 32, lq - row0,

@@ -80,32 +80,6 @@ __device__ __forceinline__ void atomic_max_float(float* addr, float v) {
     else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(addr), __float_as_uint(v));
 }
 
-// Gives a row the infinities and NaN of V that the products did without: those of the keys from
-// `first`, the first that a row of the CTA does not see, up to the last one it sees itself.  A
-// key whose values the products had as well gives the same again.
-template <int DP>
-__device__ __noinline__ void add_nonfinite(const AttnParams& p, uint32_t o_t, int first, int last, bool live, int kv_head) {
-#pragma unroll 1
-    for (int i = 0; i < DP / 32; ++i) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(o_t + 32u * i, o);
-        tmem_ld_wait();
-#pragma unroll 1
-        for (int j = first; live && j <= last; ++j) {
-            const __nv_bfloat16* v = p.v.p + (long long)j * p.v.rs + (long long)kv_head * p.v.hs + 32 * i;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (32 * i + e < p.d) {
-                    const float x = __bfloat162float(v[e]);
-                    if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-                }
-        }
-        __syncwarp();
-        tmem_st_32x32b_x32(o_t + 32u * i, o);
-    }
-    tmem_st_wait();
-}
-
 template <int DP>
 __global__ void __launch_bounds__(FwLayout<DP>::THREADS, FwLayout<DP>::CTAS)
 attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwMaps maps) {
@@ -411,7 +385,7 @@ attention_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant
                 // no key seen, or none with any weight: the sum is 0
                 const bool none = m == -INFINITY && l == l;
                 if (nw > 0 && __any_sync(0xffffffffu, *poisoned != 0))
-                    add_nonfinite<DP>(p, o_t, k0 + max(0, row0 + shift + 1), k0 + see, live, kv_head);
+                    add_nonfinite<DP / 32>(p.v, p.d, o_t, 0, 1.f, k0 + max(0, row0 + shift + 1), k0 + see, live, kv_head);
                 const float inv = none ? 0.f : 1.f / l;
                 for (int h = 0; h < 2; ++h)
                     store_rows<DP>(o_t + (uint32_t)(DP / 2 * h), nw > 0, none, inv, smem_u32(sq) + w * L::TILE, h,

@@ -104,3 +104,27 @@ def test_clip_with_infinite_logits(opt):
     opt.qk_clip(c, e, top, d, tau)
     opt.sync()
     assert not a[4 * d:].any() and torch.equal(a == 0, c == 0) and torch.equal(b == 0, e == 0)
+
+
+@pytest.mark.parametrize("hq,hk,d", [(2, 1, 128), (2, 2, 64), (2, 1, 40)])
+@pytest.mark.parametrize("at", [1, 63, 100, 127, 128, 200, 299, 555])
+def test_an_infinite_component_of_a_key_with_no_weight(opt, at, hq, hk, d):
+    """One component of key `at` is infinite and every query's is negative there: the logit is -inf, the weight 0 and
+    the log-sum finite.  By the formula dq of the queries that see the key has 0 * inf in that component, wherever the
+    key lies in its tile; the other components, and the queries before, are as if the key were not there."""
+    n = 600
+    q, k, v, do = inputs(160 + at, n, n, hq, hk, d)
+    q[:, :, 3] = -q[:, :, 3].abs() - 0.5
+    want = [t.clone() for t in run_both(opt, q, k, v, do, cu([n]), cu([n]))]
+    k[at, 0, 3] = math.inf
+    out, lse, top, dq, dk, dv = run_both(opt, q, k, v, do, cu([n]), cu([n]))
+    heads = hq // hk                                            # those that read key head 0
+    assert torch.equal(dq[:at], want[3][:at]) and torch.equal(dq[:, heads:], want[3][:, heads:])
+    assert bool(torch.isfinite(lse).all()) and bool(torch.isfinite(out).all())
+    assert not bool(torch.isfinite(dq[at:, :heads, 3]).any())
+    others = [e for e in range(d) if e != 3]
+    assert bool(torch.isfinite(dq[:, :, others]).all())
+    # key `at` of head 0 far away instead of infinitely far: the same weights
+    k[at, 0, 3] = 1e30
+    far = run_both(opt, q, k, v, do, cu([n]), cu([n]))
+    assert torch.equal(dq[:, :, others], far[3][:, :, others]) and torch.equal(out, far[0]) and torch.equal(lse, far[1])
