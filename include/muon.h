@@ -336,6 +336,19 @@ typedef struct {
 muon_status muon_validate_attention_grad(const muon_attention_grad_args* args);
 muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_args* args, void* stream);
 
+/* The same calls for outputs that hold nothing yet: rows of no sequence (in front of the
+ * first, behind the last) of those named by `fill`, a sum of MUON_FILL_ bits (OUT and LSE
+ * of the first call, DQ, DK and DV of the second), are written, too: 0, in lse -inf.  What
+ * reads all rows of them, as muon_weight_grad does, then needs no care for padding.
+ * (Where cu_seqlens are out of range, rows of good sequences may be filled as well.) */
+#define MUON_FILL_OUT 1
+#define MUON_FILL_LSE 2
+#define MUON_FILL_DQ 4
+#define MUON_FILL_DK 8
+#define MUON_FILL_DV 16
+muon_status muon_attention_fill(muon_handle* h, const muon_attention_args* args, int fill, void* stream);
+muon_status muon_attention_backward_fill(muon_handle* h, const muon_attention_grad_args* args, int fill, void* stream);
+
 /* An activation x (rows x cols) kept in 8 bits until the backward pass: blocks of
  * MUON_CKPT_BLOCK values along a row share a scale byte E, and a value is
  * code * 2^(E - 133) with an int8 code.  E is the smallest E >= 0 for which every

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libmuon_b200.so")
 
 MUON_OK, MUON_ERR_INVALID, MUON_ERR_UNSUPPORTED, MUON_ERR_OOM, MUON_ERR_CUDA, MUON_ERR_DEVICE_TIMEOUT = range(6)
 MUON_BF16, MUON_FP32 = 0, 1
+MUON_FILL_OUT, MUON_FILL_LSE, MUON_FILL_DQ, MUON_FILL_DK, MUON_FILL_DV = 1, 2, 4, 8, 16
 PREC_BF16, PREC_FP32_DEBUG = 0, 1
 SCALE_NONE, SCALE_MATCH_RMS, SCALE_CUSTOM = 0, 1, 2
 NS_GRAM, NS_POLY, NS_UPDATE = 0, 1, 2
@@ -126,6 +127,10 @@ _SIGNATURES = {
     "muon_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionArgs), ctypes.c_void_p]),
     "muon_validate_attention_grad": (ctypes.c_int, [ctypes.POINTER(_AttentionGradArgs)]),
     "muon_attention_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionGradArgs), ctypes.c_void_p]),
+    "muon_attention_fill": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionArgs), ctypes.c_int,
+                                           ctypes.c_void_p]),
+    "muon_attention_backward_fill": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(_AttentionGradArgs), ctypes.c_int,
+                                                    ctypes.c_void_p]),
     "muon_checkpoint_store": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                              ctypes.c_longlong, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "muon_checkpoint_load": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
@@ -540,30 +545,38 @@ class Muon:
         [rows, kv heads, head_dim] in bf16, cu_seqlens int32 [sequences + 1] on the device (cu_seqlens_k where the
         keys are packed otherwise), scale 1 / sqrt(head_dim) by default.  Writes out (layout of q), lse
         [heads, rows] fp32 and raises max_logits [heads] fp32 to the largest logit of each head, for qk_clip.
-        Returns (out, lse); buffers that are not given are allocated, rows of no sequence left as they are."""
+        Returns (out, lse).  Rows of no sequence are left as they are in buffers that are given, and are 0 (lse: -inf)
+        in those that the call allocates: `weight_grad` and the next projection sum over all rows."""
+        fill = 0
         if out is None:
-            out = _empty(None, None, q, stream)
+            out, fill = _empty(None, None, q, stream), MUON_FILL_OUT
         if lse is None:
             lse = _empty((q.shape[1], q.shape[0]) if q.dim() == 3 else (0,), torch.float32, q, stream)
+            fill |= MUON_FILL_LSE
         args = _AttentionArgs.from_buffer_copy(_ATTENTION_PACK.pack(
             *self._attention_fields(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, max_logits)))
-        self._check(lib().muon_attention(self._h, args, _stream(stream, self.device)), "muon_attention")
+        self._check(lib().muon_attention_fill(self._h, args, fill, _stream(stream, self.device)), "muon_attention")
         return out, lse
 
     def attention_backward(self, grad_out, q, k, v, out, lse, cu_seqlens, dq=None, dk=None, dv=None,
                            scale: Optional[float] = None, cu_seqlens_k=None, stream=None):
         """Gradients of `attention` (see muon_attention_backward) from its inputs, out and lse.  Returns
-        (dq, dk, dv); buffers that are not given are allocated, rows of no sequence left as they are."""
+        (dq, dk, dv).  Rows of no sequence are left as they are in buffers that are given, and are 0 in those that the
+        call allocates."""
         fields = self._attention_fields(q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, None)
-        dq = _empty(None, None, q, stream) if dq is None else dq
-        dk = _empty(None, None, k, stream) if dk is None else dk
-        dv = _empty(None, None, v, stream) if dv is None else dv
+        fill = 0
+        if dq is None:
+            dq, fill = _empty(None, None, q, stream), MUON_FILL_DQ
+        if dk is None:
+            dk, fill = _empty(None, None, k, stream), fill | MUON_FILL_DK
+        if dv is None:
+            dv, fill = _empty(None, None, v, stream), fill | MUON_FILL_DV
         delta = _empty(None, None, lse, stream)
         dev = self.device
         args = _AttentionGradArgs.from_buffer_copy(_ATTENTION_GRAD_PACK.pack(
             *fields, *_heads("grad_out", grad_out, q.shape, dev), *_heads("dq", dq, q.shape, dev),
             *_heads("dk", dk, k.shape, dev), *_heads("dv", dv, v.shape, dev), delta.data_ptr()))
-        self._check(lib().muon_attention_backward(self._h, args, _stream(stream, self.device)),
+        self._check(lib().muon_attention_backward_fill(self._h, args, fill, _stream(stream, self.device)),
                     "muon_attention_backward")
         return dq, dk, dv
 

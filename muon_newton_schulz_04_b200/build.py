@@ -22,7 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_b200.so")
 SOURCES = ["api.cu", "elementwise.cu", "gemm_tc.cu", "gemm_simt.cu", "plan.cpp", "noalloc.cu",
-           "attention_fwd.cu", "attention_bwd.cu", "checkpoint.cu", "weight_grad.cu"]
+           "attention_fwd.cu", "attention_bwd.cu", "attention_fill.cu", "checkpoint.cu", "weight_grad.cu"]
 HEADERS = ["kernels.cuh", "attention.cuh", "ckpt_format.cuh", "model_ops.cuh", "ptx.cuh", "plan.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

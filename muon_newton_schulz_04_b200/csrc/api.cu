@@ -426,6 +426,17 @@ AttnParams attention_params(const muon_handle* h, const muon_attention_args& a) 
     return p;
 }
 
+FillParams fill_params(const AttnParams& p) {
+    FillParams f{};
+    f.n_seqs = p.n_seqs;
+    f.d = p.d;
+    return f;
+}
+
+void add_fill(FillParams* f, const HeadView& x, float* lse, const int* cu, int heads, int total) {
+    if (total > 0) f->array[f->n++] = FillParams::Rows{x, lse, cu, heads, total};
+}
+
 int ckpt_ld(int cols) { return (cols + MUON_CKPT_BLOCK - 1) / MUON_CKPT_BLOCK * MUON_CKPT_BLOCK; }
 
 muon_status check_ckpt(const void* x, int x_dtype, int rows, int cols, long long xs, const int8_t* codes,
@@ -1530,16 +1541,26 @@ muon_status muon_validate_attention(const muon_attention_args* args) {
 }
 
 muon_status muon_attention(muon_handle* h, const muon_attention_args* a, void* stream) {
+    return muon_attention_fill(h, a, 0, stream);
+}
+
+muon_status muon_attention_fill(muon_handle* h, const muon_attention_args* a, int fill, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     std::string why;
     muon_status st = check_attention_fwd(a, &why);
     if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    if ((fill & ~(MUON_FILL_OUT | MUON_FILL_LSE)) != 0) return fail(h, MUON_ERR_INVALID, "fill: out and lse only");
     DeviceGuard dg(h->device);
     h->last_error.clear();
     NvtxRange nr("attention");
     HeadMaps maps;
     if ((st = attention_maps(h, *a, AT_FWD_BOX, &maps)) != MUON_OK) return st;
-    CUDA_TRY(h, launch_attention(attention_params(h, *a), maps, static_cast<cudaStream_t>(stream)));
+    const AttnParams p = attention_params(h, *a);
+    FillParams f = fill_params(p);
+    if (fill & MUON_FILL_OUT) add_fill(&f, p.out, nullptr, p.cu_q, p.hq, p.total_q);
+    if (fill & MUON_FILL_LSE) add_fill(&f, HeadView{}, p.lse, p.cu_q, p.hq, p.total_q);
+    CUDA_TRY(h, launch_attention_fill(f, static_cast<cudaStream_t>(stream)));
+    CUDA_TRY(h, launch_attention(p, maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }
 
@@ -1549,10 +1570,15 @@ muon_status muon_validate_attention_grad(const muon_attention_grad_args* args) {
 }
 
 muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_args* g, void* stream) {
+    return muon_attention_backward_fill(h, g, 0, stream);
+}
+
+muon_status muon_attention_backward_fill(muon_handle* h, const muon_attention_grad_args* g, int fill, void* stream) {
     if (!h) return MUON_ERR_INVALID;
     std::string why;
     muon_status st = check_attention_grad(g, &why);
     if (st != MUON_OK) return fail(h, st, "%s", why.c_str());
+    if ((fill & ~(MUON_FILL_DQ | MUON_FILL_DK | MUON_FILL_DV)) != 0) return fail(h, MUON_ERR_INVALID, "fill: dq, dk and dv only");
     DeviceGuard dg(h->device);
     h->last_error.clear();
     NvtxRange nr("attention_backward");
@@ -1563,6 +1589,11 @@ muon_status muon_attention_backward(muon_handle* h, const muon_attention_grad_ar
     HeadMaps maps;
     if ((st = attention_maps(h, g->forward, AT_BWD_BOX, &maps)) != MUON_OK) return st;
     if ((st = encode_heads(h, &maps.go, g->grad_out, p.total_q, p.hq, p.d, AT_BWD_BOX, h->d_err)) != MUON_OK) return st;
+    FillParams f = fill_params(p);
+    if (fill & MUON_FILL_DQ) add_fill(&f, p.dq, nullptr, p.cu_q, p.hq, p.total_q);
+    if (fill & MUON_FILL_DK) add_fill(&f, p.dk, nullptr, p.cu_k, p.hk, p.total_k);
+    if (fill & MUON_FILL_DV) add_fill(&f, p.dv, nullptr, p.cu_k, p.hk, p.total_k);
+    CUDA_TRY(h, launch_attention_fill(f, static_cast<cudaStream_t>(stream)));
     CUDA_TRY(h, launch_attention_backward(p, maps, static_cast<cudaStream_t>(stream)));
     return MUON_OK;
 }

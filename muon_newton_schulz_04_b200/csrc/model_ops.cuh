@@ -43,6 +43,19 @@ struct HeadMaps {
 cudaError_t launch_attention(const AttnParams& p, const HeadMaps& m, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnParams& p, const HeadMaps& m, cudaStream_t s);
 
+// Outputs whose rows of no sequence are to be filled: vectors of heads, or (lse set) one float
+// a row and head.
+struct FillParams {
+    struct Rows {
+        HeadView x;
+        float* lse;
+        const int* cu;
+        int heads, total;
+    } array[3];
+    int n, n_seqs, d;
+};
+cudaError_t launch_attention_fill(const FillParams& p, cudaStream_t s);
+
 constexpr int CKPT_BLOCK = 32;    // values that share a scale byte
 
 cudaError_t launch_checkpoint_store(const void* x, int x_bf16, int rows, int cols, long long xs, int8_t* codes,

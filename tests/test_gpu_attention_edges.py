@@ -128,3 +128,78 @@ def test_an_infinite_component_of_a_key_with_no_weight(opt, at, hq, hk, d):
     k[at, 0, 3] = 1e30
     far = run_both(opt, q, k, v, do, cu([n]), cu([n]))
     assert torch.equal(dq[:, :, others], far[3][:, :, others]) and torch.equal(out, far[0]) and torch.equal(lse, far[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_padding_of_returned_buffers(opt, d):
+    """Rows of no sequence in buffers that a call returns are 0 (lse: -inf), whatever the allocator's memory held, so
+    that weight gradients, which sum over all rows, are those of the sequences' rows."""
+    total, hq, hk = 330, 4, 2
+    q, k, v, do = inputs(170 + d, total, total, hq, hk, d)
+    c = torch.tensor([20, 120, 290], dtype=torch.int32, device="cuda")
+    inside = torch.zeros(total, dtype=torch.bool, device="cuda")
+    inside[20:290] = True
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            stale = [torch.full_like(t, math.nan) for t in (q, q, k, k)] + [torch.full((hq, total), math.nan, device="cuda")]
+            stale += [torch.full((hq, total), math.nan, device="cuda")]
+            del stale
+        out, lse = opt.attention(q, k, v, c, stream=stream)
+        grads = opt.attention_backward(do, q, k, v, out, lse, c, stream=stream)
+        torch.cuda.synchronize()
+        for t in (out, *grads):
+            assert not t[~inside].any() and bool(torch.isfinite(t).all()) and bool(t[inside].any())
+        assert bool((lse[:, ~inside] == -math.inf).all()) and bool(torch.isfinite(lse[:, inside]).all())
+    x = inputs(180, total, total, 1, 1, 128)[0].view(total, 128)
+    for g in grads:
+        dy = g.flatten(1)
+        whole = opt.weight_grad(dy, opt.checkpoint(x), torch.empty(dy.shape[1], 128, device="cuda"))
+        part = opt.weight_grad(dy[20:290], opt.checkpoint(x[20:290]), torch.empty(dy.shape[1], 128, device="cuda"))
+        opt.sync()
+        # the same sums of fp32 products in another grouping of the rows: 270 additions at most, 2^-24 each
+        assert float((whole - part).norm()) <= 270 * 2.0 ** -24 * float(part.norm())
+
+
+@pytest.mark.parametrize("bounds", [[0], [70], [0, 0], [70, 70, 70], [69, 70], [5, 6, 40, 70]])
+@pytest.mark.parametrize("d", [16, 128])
+def test_padding_only_and_in_front(opt, bounds, d):
+    """No sequence at all, empty ones, a single row, padding in front: rows of no sequence are 0, lse -inf there, for
+    the buffers that the call makes, and stay in those that it is given."""
+    q, k, v, do = inputs(175, 70, 70, 4, 2, d)
+    c = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    inside = torch.zeros(70, dtype=torch.bool, device="cuda")
+    inside[bounds[0]:bounds[-1]] = True
+    want = run_both(opt, q, k, v, do, c, c)
+    torch.cuda.synchronize()
+    stale = [torch.full_like(t, math.nan) for t in (q, q, k, k)] + [torch.full((4, 70), math.nan, device="cuda")] * 2
+    del stale
+    out, lse = opt.attention(q, k, v, c)
+    grads = opt.attention_backward(do, q, k, v, out, lse, c)
+    kept = torch.full_like(k, 7.0)
+    dq, dk, dv = opt.attention_backward(do, q, k, v, out, lse, c, dk=kept)
+    opt.sync()
+    for t in (out, *grads, dq, dv):
+        assert not t[~inside].any()
+    assert bool((lse[:, ~inside] == -math.inf).all()) and dk is kept and bool((dk[~inside] == 7).all())
+    for x, y in zip((out, *grads, dk), (want[0], *want[3:], want[4])):
+        assert torch.equal(x[inside], y[inside])
+    assert torch.equal(lse[:, inside], want[1][:, inside])
+
+
+def test_fill_of_other_buffers_is_refused(opt):
+    """`fill` names outputs of its own call only."""
+    q, k, v, do = inputs(176, 8, 8, 1, 1, 64)
+    c = cu([8])
+    out, lse = opt.attention(q, k, v, c)
+    fields = opt._attention_fields(q, k, v, c, None, None, out, lse, None)
+    args = mb._AttentionArgs.from_buffer_copy(mb._ATTENTION_PACK.pack(*fields))
+    for fill in (-1, mb.MUON_FILL_DQ, 64):
+        assert mb.lib().muon_attention_fill(opt._h, args, fill, None) == mb.MUON_ERR_INVALID
+    h = mb._heads("q", q, q.shape, opt.device)
+    dq, dk, dv, delta = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q), torch.empty_like(lse)
+    grad = mb._AttentionGradArgs.from_buffer_copy(mb._ATTENTION_GRAD_PACK.pack(
+        *fields, *h, *(x for t in (dq, dk, dv) for x in mb._heads("t", t, q.shape, opt.device)), delta.data_ptr()))
+    for fill in (-1, mb.MUON_FILL_OUT, 64):
+        assert mb.lib().muon_attention_backward_fill(opt._h, grad, fill, None) == mb.MUON_ERR_INVALID
+    opt.sync()
