@@ -372,9 +372,9 @@ muon_status muon_checkpoint_load(muon_handle* h, const int8_t* codes, const uint
  * (accumulate = 1), x^ the value of the checkpoint (tokens x cols) and dy the bf16
  * gradient of y (tokens x rows; row t at dy + t * dy_stride elements, dy_stride >= rows).
  * G is the rows x cols gradient that muon_step reads, fp32 or bf16, dense; sums are
- * fp32 and G is rounded once.  tokens may be 0.  workspace: device scratch of at least
- * muon_weight_grad_workspace() bytes, 16-byte aligned (NULL when that is 0).  The same
- * inputs give the same bits. */
+ * fp32 and G is rounded once.  tokens may be 0; tokens, rows and cols are at most 2^30.
+ * workspace: device scratch of at least muon_weight_grad_workspace() bytes, 16-byte
+ * aligned (NULL when that is 0).  The same inputs give the same bits. */
 typedef struct {
     int tokens, rows, cols;
     const void* dy;

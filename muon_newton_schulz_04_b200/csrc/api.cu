@@ -459,7 +459,11 @@ muon_status check_wgrad_shape(const muon_weight_grad_args* a, std::string* why) 
     if (!a) { *why = "args is NULL"; return MUON_ERR_INVALID; }
     if (a->tokens < 0 || a->rows <= 0 || a->cols <= 0) { *why = "tokens must be >= 0, rows and cols > 0"; return MUON_ERR_INVALID; }
     if ((long long)a->rows * a->cols > (1ll << 31) - 1) { *why = "a matrix may hold at most 2^31-1 elements"; return MUON_ERR_INVALID; }
-    if (a->tokens > (1 << 30)) { *why = "too many tokens"; return MUON_ERR_UNSUPPORTED; }
+    // (rounded up to tiles and blocks in 32 bits)
+    if (a->tokens > (1 << 30) || a->rows > (1 << 30) || a->cols > (1 << 30)) {
+        *why = "tokens, rows and cols may be at most 2^30";
+        return MUON_ERR_UNSUPPORTED;
+    }
     if (a->tokens > 1 && (a->dy_stride < a->rows || a->dy_stride >= (1ll << 38))) { *why = "dy_stride must be >= rows"; return MUON_ERR_INVALID; }
     return MUON_OK;
 }
