@@ -1522,7 +1522,7 @@ muon_status muon_qk_clip_grouped(muon_handle* h, float* Wq, float* Wk, const flo
     if (!Wq || !Wk || !max_logits) return fail(h, MUON_ERR_INVALID, "Wq, Wk and max_logits are required");
     if (n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || cols <= 0) return fail(h, MUON_ERR_INVALID, "sizes must be > 0");
     if (n_heads % n_kv_heads != 0) return fail(h, MUON_ERR_INVALID, "n_heads must be a multiple of n_kv_heads");
-    if (n_heads + n_kv_heads > 65535) return fail(h, MUON_ERR_UNSUPPORTED, "at most 65535 heads");
+    if ((long long)n_heads + n_kv_heads > 65535) return fail(h, MUON_ERR_UNSUPPORTED, "at most 65535 heads");
     if ((long long)n_heads * head_dim > (1ll << 31) - 1 || (long long)n_heads * head_dim * cols > (1ll << 31) - 1)
         return fail(h, MUON_ERR_INVALID, "matrix too large");
     if (!(finite(tau) && tau > 0.f)) return fail(h, MUON_ERR_INVALID, "tau must be finite and > 0");

@@ -203,3 +203,14 @@ def test_fill_of_other_buffers_is_refused(opt):
     for fill in (-1, mb.MUON_FILL_OUT, 64):
         assert mb.lib().muon_attention_backward_fill(opt._h, grad, fill, None) == mb.MUON_ERR_INVALID
     opt.sync()
+
+
+def test_clip_of_too_many_heads_is_refused(opt):
+    """More heads than a grid has rows, up to sums of heads that leave 32 bits: refused before anything is launched."""
+    w = torch.ones(64, device="cuda")
+    p = w.data_ptr()
+    for hq, hk in ((65535, 1), (32768, 32768), ((1 << 31) - 1, (1 << 31) - 1), ((1 << 31) - 1, 1), (1 << 30, 1 << 30)):
+        st = mb.lib().muon_qk_clip_grouped(opt._h, p, p + 128, p + 64, hq, hk, 1, 1, 1.0, None)
+        assert st == mb.MUON_ERR_UNSUPPORTED, (hq, hk)
+    opt.sync()
+    assert bool((w == 1).all())
