@@ -287,7 +287,9 @@ typedef struct {
  * counts, and a row with a NaN logit, unless another is +inf, is passed over).  A logit of
  * -inf has weight 0; a query whose logits all are -inf gets O = 0 and lse = -inf.
  * out, lse and max_logits may not overlap any buffer of the call
- * (strided views that interleave without sharing an element do not overlap).
+ * (views of one array at the same strides that share no element do not overlap: column
+ * ranges of its rows, or q, k and v head by head; ranges that interleave in other ways may
+ * be refused).
  * Non-finite values reach the outputs of the queries that see them and no others: not
  * those of earlier queries, nor of another sequence.
  * cu_seqlens values outside the rule above are seen by the kernels only: such a

@@ -292,26 +292,52 @@ muon_status check_groups(const muon_group* g, int n, std::string* why) {
 
 // ---- operators between a layer's forward pass and its step: host checks ----
 
-// Bytes [base, base + extent) that a strided array of a call touches; when row > 0 it
-// touches only [base + i * row, + width) for i < rows, width <= row.
+// What an array of a call touches of [base, base + extent): vectors of `width` bytes, `count`
+// of them at the one stride and at the other (outer > inner; 0: a single one).
 struct Extent {
     uintptr_t base = 0;
-    size_t extent = 0, row = 0, width = 0;
+    size_t extent = 0, width = 0;
+    size_t outer = 0, outer_count = 1, inner = 0, inner_count = 1;
     bool written = false;
     const char* name = "";
 };
 
 Extent flat(const void* p, size_t bytes, bool written, const char* name) {
-    return Extent{reinterpret_cast<uintptr_t>(p), bytes, 0, 0, written, name};
+    Extent e;
+    e.base = reinterpret_cast<uintptr_t>(p);
+    e.extent = e.width = bytes;
+    e.written = written;
+    e.name = name;
+    return e;
+}
+
+// Bytes that the array covers of each period of m bytes, beginning at base modulo m, when the
+// strides that are multiples of m are taken out.
+size_t span(const Extent& e, size_t m) {
+    return e.width + (e.outer % m != 0 ? (e.outer_count - 1) * e.outer : 0) + (e.inner % m != 0 ? (e.inner_count - 1) * e.inner : 0);
+}
+
+// Whether `wb` bytes from `off` on and `wa` bytes from 0 on share none, both repeated every m.
+bool apart(size_t off, size_t wa, size_t wb, size_t m) {
+    off %= m;
+    return off >= wa && off + wb <= m;
 }
 
 bool share_memory(const Extent& x, const Extent& y) {
     const Extent &a = x.base <= y.base ? x : y, &b = x.base <= y.base ? y : x;
     if (a.extent == 0 || b.extent == 0 || a.base + a.extent <= b.base) return false;
-    // views of one row-major array: disjoint column ranges do not meet
-    if (a.row > 0 && a.row == b.row) {
-        const size_t off = (b.base - a.base) % a.row;
-        if (off >= a.width && off + b.width <= a.row) return false;
+    // views of one larger array: disjoint columns of its rows, or of its heads
+    const size_t off = b.base - a.base;
+    for (const size_t m : {a.outer, a.inner, b.outer, b.inner})
+        if (m > 0 && apart(off, span(a, m), span(b, m), m)) return false;
+    // the same strides, rows no multiple of the heads': a row of b beside the one of a that begins
+    // last in front of it, and beside the next, if there is one
+    const size_t m = a.outer, h = a.inner;
+    if (h > 0 && m == b.outer && h == b.inner) {
+        const size_t at = off % m;
+        const bool same = at >= span(a, m) || apart(at, a.width, b.width, h);
+        const bool next = at + span(b, m) <= m || off / m + 1 >= a.outer_count || apart(m - at, b.width, a.width, h);
+        if (same && next) return false;
     }
     return true;
 }
@@ -347,7 +373,12 @@ muon_status check_heads(const muon_heads& v, int rows, int heads, int d, bool wr
         return MUON_ERR_UNSUPPORTED;
     }
     *e = flat(v.ptr, 2 * (size_t)((rows - 1) * rs + (heads - 1) * hs + d), written, name);
-    if (by_row && rows > 1) { e->row = 2 * (size_t)rs; e->width = 2 * (size_t)((heads - 1) * hs + d); }
+    e->width = 2 * (size_t)d;
+    const bool rows_outside = rs > hs;
+    e->outer = 2 * (size_t)(rows_outside ? rs : hs);
+    e->inner = 2 * (size_t)(rows_outside ? hs : rs);
+    e->outer_count = rows_outside ? rows : heads;
+    e->inner_count = rows_outside ? heads : rows;
     return MUON_OK;
 }
 

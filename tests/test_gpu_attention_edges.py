@@ -214,3 +214,31 @@ def test_clip_of_too_many_heads_is_refused(opt):
         assert st == mb.MUON_ERR_UNSUPPORTED, (hq, hk)
     opt.sync()
     assert bool((w == 1).all())
+
+
+@pytest.mark.parametrize("rows_first", [True, False])
+@pytest.mark.parametrize("ql,h,d", [([150, 3, 260], 4, 64), ([77, 300], 3, 128), ([1], 5, 8)])
+def test_views_interleaved_head_by_head(opt, ql, h, d, rows_first):
+    """q, k and v (dq, dk and dv) of an array whose heads lie as q, k, v, q, k, v, ...: the same bits as dense ones, and
+    nothing written beside them."""
+    t = sum(ql)
+    q, k, v, do = inputs(210 + d, t, t, h, h, d)
+    want = run_both(opt, q, k, v, do, cu(ql), cu(ql))
+
+    def parts():
+        x = torch.full((t, h, 4, d) if rows_first else (h, t, 4, d), 7.0, dtype=q.dtype, device="cuda")
+        return x, [(x if rows_first else x.transpose(0, 1))[:, :, i] for i in range(4)]
+
+    fused, views = parts()
+    for a, b in zip(views, (q, k, v)):
+        a.copy_(b)
+    out, lse = opt.attention(*views[:3], cu(ql), out=views[3])
+    grads, g = parts()
+    opt.attention_backward(do, *views[:3], out, lse, cu(ql), dq=g[0], dk=g[1], dv=g[2])
+    opt.sync()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for a, b in zip(g, want[3:]):
+        assert torch.equal(a, b)
+    for a, b in zip(views, (q, k, v)):
+        assert torch.equal(a, b)
+    assert bool((g[3] == 7).all())
