@@ -256,6 +256,12 @@ def _check_dense(name: str, t, device: int):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_sizes(name: str, *sizes: int):
+    """The C library takes sizes as int, and ctypes would cut larger ones off without a word."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"{name}: sizes must be below 2^31, got {' x '.join(map(str, sizes))}")
+
+
 def _heads(name: str, t, shape, device: int):
     """(address, row stride, head stride) of a bf16 CUDA tensor [rows, heads, head_dim] of the given shape with a
     dense last dimension."""
@@ -509,6 +515,7 @@ class Muon:
             raise ValueError("Wq and Wk must be 2-D with the same number of columns")
         if head_dim <= 0 or Wq.shape[0] != n_heads * head_dim or Wk.shape[0] % head_dim != 0 or Wk.shape[0] == 0:
             raise ValueError("Wq must have n_heads * head_dim rows, Wk a multiple of head_dim")
+        _check_sizes("Wq", *Wq.shape)
         self._check(lib().muon_qk_clip_grouped(self._h, Wq.data_ptr(), Wk.data_ptr(), max_logits.data_ptr(), n_heads,
                                                Wk.shape[0] // head_dim, head_dim, Wq.shape[1], float(tau),
                                                ctypes.c_void_p(_stream(stream, self.device))), "muon_qk_clip_grouped")
@@ -585,6 +592,7 @@ class Muon:
         stride = _check_rows("x", x, self.device)
         code = _dtype_code(x)
         rows, cols = x.shape
+        _check_sizes("x", rows, cols)
         if ckpt is None:
             blocks = -(-cols // CKPT_BLOCK)
             ckpt = Checkpoint(_empty((rows, blocks * CKPT_BLOCK), torch.int8, x, stream),
@@ -602,6 +610,7 @@ class Muon:
         """The values of a checkpoint, written to `out` (bf16 or fp32, dense rows; bf16 when not given)."""
         _check_checkpoint(ckpt, self.device)
         rows, cols = ckpt.rows, ckpt.cols
+        _check_sizes("the checkpoint", rows, cols)
         if out is None:
             out = _empty((rows, cols), torch.bfloat16, ckpt.codes, stream)
         stride = _check_rows("out", out, self.device)
@@ -621,6 +630,7 @@ class Muon:
         if dy.dtype is not torch.bfloat16:
             raise TypeError(f"dy: unsupported dtype {dy.dtype}, expected torch.bfloat16")
         tokens, rows = dy.shape
+        _check_sizes("weight_grad", tokens, rows, ckpt.cols)
         if tokens != ckpt.rows:
             raise ValueError(f"dy has {tokens} rows, the checkpoint {ckpt.rows}")
         if tuple(G.shape) != (rows, ckpt.cols):

@@ -242,3 +242,19 @@ def test_views_interleaved_head_by_head(opt, ql, h, d, rows_first):
     for a, b in zip(views, (q, k, v)):
         assert torch.equal(a, b)
     assert bool((g[3] == 7).all())
+
+
+def test_sizes_past_32_bits_are_refused(opt):
+    """A row of 2^32 + 5 values is refused, not taken for one of 5."""
+    n = (1 << 32) + 5
+    x = torch.empty(1, n, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        opt.checkpoint(x)
+    dy = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda")
+    c = opt.checkpoint(torch.ones(1, 1, device="cuda"))
+    with pytest.raises(ValueError):
+        opt.weight_grad(dy, c, x.view(n, 1))
+    w = torch.empty(1, (1 << 32) + 5, device="cuda")
+    with pytest.raises(ValueError):
+        opt.qk_clip_grouped(w, w, torch.ones(1, device="cuda"), 1, 1.0)
+    opt.sync()
