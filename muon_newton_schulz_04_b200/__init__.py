@@ -541,8 +541,10 @@ class Muon:
             if max_logits.dtype is not torch.float32 or max_logits.shape != (hq,):
                 raise ValueError(f"max_logits must be float32 of shape {(hq,)}")
             _check_dense("max_logits", max_logits, dev)
+        if scale is None:
+            scale = d ** -0.5 if d > 0 else 1.0         # (heads without width are refused by the library)
         kv = (tk, hk, d)
-        return (n - 1, hq, hk, d, tq, tk, cu_seqlens.data_ptr(), cu_k.data_ptr(), d ** -0.5 if scale is None else scale,
+        return (n - 1, hq, hk, d, tq, tk, cu_seqlens.data_ptr(), cu_k.data_ptr(), scale,
                 *_heads("q", q, q.shape, dev), *_heads("k", k, kv, dev), *_heads("v", v, kv, dev),
                 *_heads("out", out, q.shape, dev), lse.data_ptr(), 0 if max_logits is None else max_logits.data_ptr())
 

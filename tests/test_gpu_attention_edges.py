@@ -258,3 +258,18 @@ def test_sizes_past_32_bits_are_refused(opt):
     with pytest.raises(ValueError):
         opt.qk_clip_grouped(w, w, torch.ones(1, device="cuda"), 1, 1.0)
     opt.sync()
+
+
+def test_scales_and_widths_outside_their_types(opt):
+    """A scale above fp32's range and heads without width are refused by the library, as other arguments are."""
+    q, k, v, do = inputs(220, 8, 8, 1, 1, 64)
+    c = cu([8])
+    out, lse = opt.attention(q, k, v, c)
+    e = torch.empty(8, 1, 0, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: opt.attention(q, k, v, c, scale=1e39), lambda: opt.attention(e, e, e, c),
+                 lambda: opt.attention_backward(do, q, k, v, out, lse, c, scale=1e39),
+                 lambda: opt.attention_backward(e, e, e, e, e, lse, c)):
+        with pytest.raises(mb.MuonError) as err:
+            call()
+        assert err.value.status == mb.MUON_ERR_INVALID
+    opt.sync()
