@@ -205,6 +205,54 @@ def test_fill_of_other_buffers_is_refused(opt):
     opt.sync()
 
 
+def test_rows_of_bad_sequences_stay(opt):
+    """Bounds out of range: the forward and the gradient kernels leave the rows of such a sequence as they were,
+    compute the good one to the same bits as alone, and report it."""
+    q, k, v, do = inputs(190, 64, 64, 2, 1, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for bad, good in (([0, 20, 65], (0, 20)), ([0, 30, 20], (0, 30)), ([-1, 20, 64], (20, 64))):
+        want = run_both(opt, q, k, v, do, torch.tensor(good, **i32), torch.tensor(good, **i32))
+        c = torch.tensor(bad, **i32)
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 64), 7.0, device="cuda")
+        top = torch.full((2,), -math.inf, device="cuda")
+        opt.attention(q, k, v, c, out=out, lse=lse, max_logits=top)
+        with pytest.raises(mb.MuonError) as e:
+            opt.sync()
+        assert e.value.status == mb.MUON_ERR_INVALID
+        grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+        opt.attention_backward(do, q, k, v, out, lse, c, dq=grads[0], dk=grads[1], dv=grads[2])
+        with pytest.raises(mb.MuonError) as e:
+            opt.sync()
+        assert e.value.status == mb.MUON_ERR_INVALID
+        # (rows outside the good sequence hold 7 in `want`, too)
+        for name, got, ref in zip(("out", "lse", "top", "dq", "dk", "dv"), [out, lse, top] + grads, want):
+            assert torch.equal(got, ref), (name, bad)
+    opt.sync()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_at_large_logits(opt, d):
+    """dq and dk where S - lse cancels.  Logits / scale reach 2^13; five or nine accumulations of 16 columns, each off
+    by at most 2^-23 of that, move S and lse by 9 * 2^-10 * scale <= 2^-9.8 each, so P, and with it dS, by a factor
+    within 1 + 2^-8.8: on top of the other test's tolerance, 2^-8.8 of the sum of the terms' magnitudes."""
+    n, scale = 300, d ** -0.5
+    q, k, v, do = inputs(200 + d, n, n, 2, 2, d)
+    q, k = (q.float() * 8).to(torch.bfloat16), (k.float() * 8).to(torch.bfloat16)
+    out, lse, top, dq, dk, dv = run_both(opt, q, k, v, do, cu([n]), cu([n]))
+    ro, rl, rt, rq, rk, rv = reference(q, k, v, [n], [n], scale, do)
+    assert 150 < float(rt.max()) and float(rt.max()) / scale < 2.0 ** 13
+    Q, K, V, G = (t.double().transpose(0, 1) for t in (q, k, v, do))
+    S = (Q @ K.transpose(1, 2) * scale).masked_fill(~torch.ones(n, n, dtype=torch.bool, device="cuda").tril(), -math.inf)
+    P = torch.softmax(S, 2)
+    dS = (P * (G @ V.transpose(1, 2) - (G * (P @ V)).sum(2, keepdim=True))).abs() * scale
+    # (`close` weighs what comes beside the gradient with 2^-8)
+    more = 2.0 ** -0.8
+    mq, mk = (dS @ K.abs()).transpose(0, 1) * more, (dS.transpose(1, 2) @ Q.abs()).transpose(0, 1) * more
+    close(dq, (rq[0], rq[1] + mq), TOL_GRAD, "dq")
+    close(dk, (rk[0], rk[1] + mk), TOL_GRAD, "dk")
+    close(dv, (rv[0], 2.0 ** -0.8 * (P.transpose(1, 2) @ G.abs()).transpose(0, 1)), TOL_GRAD, "dv")
+
+
 def test_clip_of_too_many_heads_is_refused(opt):
     """More heads than a grid has rows, up to sums of heads that leave 32 bits: refused before anything is launched."""
     w = torch.ones(64, device="cuda")
@@ -273,3 +321,36 @@ def test_scales_and_widths_outside_their_types(opt):
             call()
         assert err.value.status == mb.MUON_ERR_INVALID
     opt.sync()
+
+
+@pytest.mark.parametrize("d,power", [(64, -61), (64, -20), (64, 30), (64, 67), (16, -62), (16, 66)])
+def test_scales_at_their_limits(opt, d, power):
+    """q times 2^-n with a scale 2^n times as large, up to the scales' limits 2^-64 and 2^64: every product, sum and
+    rounding is the same times a power of two, so the same bits; dq is 2^n times as large."""
+    n, base = [150, 43], d ** -0.5
+    assert math.frexp(base)[0] == 0.5 and 2.0 ** -64 <= base * 2.0 ** power <= 2.0 ** 64
+    q, k, v, do = inputs(230 + d, 193, 193, 4, 2, d)
+    want = run_both(opt, q, k, v, do, cu(n), cu(n), scale=base)
+    got = run_both(opt, (q.double() * 2.0 ** -power).to(torch.bfloat16), k, v, do, cu(n), cu(n), scale=base * 2.0 ** power)
+    for name, i in (("out", 0), ("lse", 1), ("top", 2), ("dk", 4), ("dv", 5)):
+        assert torch.equal(got[i], want[i]), name
+    assert torch.equal(got[3].double(), want[3].double() * 2.0 ** power)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -128, 2.0 ** -120, 2.0 ** 120, 2.0 ** 125])
+@pytest.mark.parametrize("t,r,n", [(300, 70, 100), (1100, 130, 40)])
+def test_weight_grad_of_the_smallest_and_largest_activations(opt, t, r, n, size):
+    """Activations whose blocks have units below 2^-126, where the values of a checkpoint are subnormal, and near the
+    largest: as exact as any others.  The tolerance of the other tests: sums in fp32, 2^-23 * sqrt(tokens)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(240 + t)
+    x = torch.randn(t, n, generator=gen, device="cuda").clamp(-3.9, 3.9).double() * size
+    dy = (torch.randn(t, r, generator=gen, device="cuda").double() / size).clamp(-1e38, 1e38).to(torch.bfloat16)
+    c = opt.checkpoint(x.to(torch.bfloat16))
+    G = opt.weight_grad(dy, c, torch.empty(r, n, device="cuda"))
+    opt.sync()
+    unit = torch.tensor([2.0 ** (e - 133) for e in range(255)], dtype=torch.float64, device="cuda")[c.scales.long()]
+    values = (c.codes.double() * unit.repeat_interleave(32, 1))[:, :n]
+    want = dy.double().t() @ values
+    assert float(want.abs().max()) > 1e-3
+    assert float((G.double() - want).norm() / want.norm()) <= 2.0 ** -23 * math.sqrt(16384)
