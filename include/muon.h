@@ -279,7 +279,8 @@ typedef struct {
  * A query that sees no key gets O = 0 and lse = -inf.  Rows that belong to no
  * sequence (between sequences, behind the last) are not written.  Sums, softmax
  * statistics and products are accumulated in fp32; the exponentials enter the second
- * product rounded to bf16.
+ * product rounded to bf16.  Their sum divides O at the end: |v| times 2^8 times the number
+ * of keys has to stay within fp32's range.
  *
  * head_dim: a multiple of 8, at most 128.  scale: 2^-64 to 2^64.  q, k, v: read; out:
  * written; lse: fp32 [n_heads][total_q], written; max_logits: n_heads floats or NULL,
@@ -327,6 +328,9 @@ muon_status muon_attention(muon_handle* h, const muon_attention_args* args, void
  * the keys that it sees, as the formulas carry them (a key with a logit of -inf has weight
  * 0, and an infinite component of it reaches that component of dq alone), and no other
  * gradient.
+ * dq is formed with D_i of `out` as it is given, rounded to bf16; dk, and dq where the 128
+ * queries around i see at most 64 keys (128, for head_dim above 64), with
+ * D_i = sum_j P_ij (grad_out_i . v_j), which is the same without that rounding.
  * dq, dk, dv and delta may not overlap any buffer of the call. */
 typedef struct {
     muon_attention_args forward;

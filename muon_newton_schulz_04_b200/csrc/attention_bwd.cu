@@ -26,11 +26,17 @@
 // tensor memory, so two CTAs an SM, four such warps each, which also hide each other's start
 // and end (eight sequences of 1024, 25 heads: 225 us with one CTA an SM, 188 with two).
 //
+// D comes from O as the forward pass rounded it, off by up to 2^-8 sum_d |dO_id O_id|.  The first
+// kernel finds the exact one as it goes, D + sum_j dS_ij, since sum_j P_ij = 1, and leaves that
+// for the second.  For its own dS that comes too late (to mend dQ afterwards would take
+// sum_j P_ij k_j, a product more), but where a row block sees one step of keys, when D's
+// rounding counts most, P and dP of all its keys are at hand and D is formed from them.
+//
 // Two spare warps take infinities and NaN out of K, Q and dO in the tiles that not every row
-// sees all of (there 0 times them would reach rows that do not see them): 199 us instead of
-// 188.  8192 rows in 5 sequences, 32 heads over 8 of 128: 1030 us at full clocks (443 and 587),
+// sees all of (there 0 times them would reach rows that do not see them): 199-211 us instead of
+// 188.  8192 rows in 5 sequences, 32 heads over 8 of 128: 1030 us at full clocks (443 and 587;
 // 0.87 PFLOP/s by the formula's five products, 1.2 by the seven formed, where the sustained
-// rate of plain products is 1.38.
+// rate of plain products is 1.38) to 1230 under the power cap.
 #include <algorithm>
 
 #include "attention.cuh"

@@ -15,13 +15,17 @@
 //
 // The special function unit takes 8 cycles for a warp's exponentials, 1024 for 128 x 128: as
 // long as the two products of a 128-wide head take, twice as long as those of a 64-wide one.
-// So a quarter of them is computed on the FMA pipe (exp2_pair), at 12 cycles a warp; the best
-// mix of the two gets to 7.5 where the unit alone gets to 8.6.
+// So a quarter of a 64-wide head's and an eighth of a 128-wide one's are computed on the FMA
+// pipe (exp2_pair), at 12 cycles a warp; the best mix of the two gets to 7.5 where the unit
+// alone gets to 8.6.
 //
 // One B200: 8192 rows in 5 sequences (the longest 6500), 32 heads over 8 of 128: 338 us at full
-// clocks, 1.05 PFLOP/s, tensor pipe 52 % and special function unit 45 % of the cycles.  8
-// sequences of 1024, 25 heads of 64: 66 us; a CTA has 4.5 key tiles there, and its start and end
-// take as long as they do.
+// clocks (1.05 PFLOP/s, tensor pipe 52 % and special function unit 45 % of the cycles) to 396
+// under the power cap.  8 sequences of 1024, 25 heads of 64: 66-74 us; a CTA has 4.5 key tiles
+// there, and its start and end take as long as they do.
+//
+// O is divided by the sum of P at the end, so values beyond fp32's range / (2^8 keys) overflow
+// where their mean would not.
 //
 // P is 0 where a row does not see a key (exp2_pair and ex2 both give 0 for -inf), but 0 times
 // an infinity or a NaN is not: a spare warp takes those out of V in the tiles that not every

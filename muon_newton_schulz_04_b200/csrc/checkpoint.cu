@@ -9,10 +9,11 @@
 //
 // Bound by memory: store reads 2 or 4 bytes and writes 33/32 a value, load the reverse.
 // Two lanes share a block (16 values each), so codes move 16 bytes a lane; where the rows of x
-// do not start on 16-byte addresses, a warp takes blocks, one value of each a lane.  16384 x 4096 bf16
-// on one B200: written in 33 us, read back in 34 (201 MB each, 6.1 and 5.9 TB/s of the 6.56
-// TB/s of a copy).  What it took: no integer conversion (a quarter of the rate), no 64-bit
-// division, maxima two bf16 at a time.
+// do not start on 16-byte addresses, a warp takes blocks, one value of each a lane.  16384 x
+// 4096 bf16 on one B200: written in 33 us, read back in 34 (201 MB each, 6.1 and 5.9 TB/s of
+// the 6.56 TB/s of a copy); fp32 49 and 72 us (floor 51 each).  16384 x 3999, a value or a code
+// an access: bf16 76 and 54 us (floor 30 each), fp32 73 and 69 (50).  What it took: no integer
+// conversion (a quarter of the rate), no 64-bit division, maxima two bf16 at a time.
 #include <algorithm>
 
 #include "ckpt_format.cuh"

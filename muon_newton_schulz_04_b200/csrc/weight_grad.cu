@@ -12,10 +12,11 @@
 // every cluster has work; their fp32 partial sums go through the caller's workspace and a
 // second kernel adds them in order (no atomics: the same inputs give the same bits).
 //
-// One B200: 8191 tokens into 4096 x 4096 234 us, 1.17 PFLOP/s; bound by shared memory, where a
-// stage's codes, its converted operand and both operands of the products take 640 cycles and
-// the products 512 (192 us with the conversion left out).  16384 tokens into 768 x 768: 31 us,
-// of which 6 join the partial sums of its 9 tiles, split in 8.
+// One B200: 8191 tokens into 4096 x 4096 234 us at full clocks (1.17 PFLOP/s) to 292 under the
+// power cap; bound by shared memory, where a stage's codes, its converted operand and both
+// operands of the products take 640 cycles and the products 512 (192 us with the conversion
+// left out).  16384 tokens into 768 x 768: 31 us, of which 6 join the partial sums of its 9
+// tiles, split in 8.
 #include <algorithm>
 
 #include "kernels.cuh"
